@@ -70,7 +70,9 @@ extern "C" {
 
 typedef enum fff_dtype {
     FFF_DTYPE_F32 = 0,
-    FFF_DTYPE_BF16 = 1
+    FFF_DTYPE_BF16 = 1,
+    FFF_DTYPE_E4M3 = 2 /* 8-bit float (OCP: 4 exponent, 3 mantissa bits): the norm's
+                          output and the optimiser's states only */
 } fff_dtype_t;
 
 typedef enum fff_status {
@@ -402,6 +404,150 @@ fff_status_t fff_forward_static(const fff_shape_t *shape, const fff_plan_t *plan
                                 const void *V_node, const void *W_out, void *y,
                                 int32_t *path_out, hipStream_t stream,
                                 const fff_stage_events_t *events);
+
+/*
+ * Around the layer: norm and optimiser
+ * ------------------------------------
+ * What a pre-norm block and its training step need beside the layer itself:
+ * the root-mean-square norm with the residual's addition and its backward
+ * pass, the AdamW step over many tensors, and the gradient's norm.  The rules
+ * above hold: dense row-major device tensors, caller-owned workspaces, no
+ * state, validation before any HIP call.  Pointers need an element's
+ * alignment only (workspaces 256 bytes), so tensors may be views that start
+ * anywhere in a buffer.
+ *
+ * Rows x [T,d] of type `dtype`, a residual stream of type `stream_dtype`
+ * (`dtype`, or FFF_DTYPE_F32 beside a bf16 layer):
+ *   z    = x + residual               (either may be NULL, not both)
+ *   rstd = 1 / sqrt(mean(z^2) + eps)
+ *   y    = z * rstd * (weight + weight_offset)
+ * y is formed from the 32-bit z; residual_out holds z rounded to
+ * stream_dtype.
+ *
+ * With out_dtype FFF_DTYPE_E4M3, y is held in 8 bits: for every row (group
+ * 0) or every `group` columns of a row (32, 64 or 128; the last group may be
+ * short) scale = max(largest |y| / 448, 2^-126) and the stored value is
+ * y / scale to nearest.  A NaN in a group makes its scale NaN; a group whose
+ * largest size is infinite has scale infinity.
+ */
+typedef struct fff_norm_shape {
+    int64_t T;             /* rows, 0 <= T < 2^31 */
+    int32_t d;             /* width, 1 <= d <= 32768 (FFF_ERROR_NOT_SUPPORTED beyond) */
+    int32_t dtype;         /* F32 or BF16: x, weight, y (unless 8 bits), dy, dx */
+    int32_t stream_dtype;  /* `dtype` or F32: residual, residual_out, z, dresidual, dz */
+    int32_t out_dtype;     /* `dtype` or E4M3 (the backward pass ignores it) */
+    int32_t group;         /* columns per scale with E4M3, else 0 */
+    float eps;             /* >= 0 */
+    float weight_offset;   /* 0, or 1 for weights kept as their difference from 1 */
+} fff_norm_shape_t;
+
+/*
+ *   x             [T,d] dtype, or NULL
+ *   residual      [T,d] stream_dtype, or NULL
+ *   weight        [d] dtype, or NULL for ones
+ *   y             [T,d] out_dtype
+ *   scale         [T, ceil(d / group)] float32 ([T] with group 0); E4M3 only
+ *   residual_out  [T,d] stream_dtype, or NULL
+ *   rstd          [T] float32 for the backward pass, or NULL
+ * residual_out may be the residual's own buffer, and any output may be the
+ * buffer of an input of its type; other overlaps are not allowed.  One
+ * launch; T = 0 is a no-op.
+ */
+fff_status_t fff_rms_norm(const fff_norm_shape_t *shape, const void *x, const void *residual,
+                          const void *weight, void *y, float *scale, void *residual_out,
+                          float *rstd, hipStream_t stream);
+
+/*
+ * Gradients of sum(y * dy) + sum(residual_out * dresidual).  With z and rstd
+ * as the forward pass left them and g = dy * (weight + weight_offset):
+ *   dz = rstd * (g - z * rstd * mean(g * z * rstd)) + dresidual
+ *   dweight = sum over rows of dy * z * rstd
+ * dz is the gradient of x and of the residual alike.
+ *   dy         [T,d] dtype           z          [T,d] stream_dtype
+ *   weight     [d] dtype or NULL     rstd       [T] float32
+ *   dresidual  [T,d] stream_dtype, or NULL
+ *   dz         [T,d] stream_dtype out
+ *   dx         [T,d] dtype out: dz rounded to the layer's type, or NULL
+ *   dweight    [d] float32 out, or NULL
+ * Rows are summed in a fixed order: results are the same on every call.  dz
+ * and dx may be the buffers of inputs of their types.  T = 0 gives dweight 0.
+ * The workspace is for dweight: without it, it may be NULL.
+ */
+fff_status_t fff_rms_norm_backward_workspace_size(const fff_norm_shape_t *shape, size_t *bytes);
+fff_status_t fff_rms_norm_backward(const fff_norm_shape_t *shape, const void *dy, const void *z,
+                                   const void *weight, const float *rstd, const void *dresidual,
+                                   void *dz, void *dx, float *dweight, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * AdamW (decoupled weight decay) over any number of tensors:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g           v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * with lr = config.lr * lr_scale of the tensor.  Every product and sum is
+ * rounded to 32 bits on its own, in this order.  Tensors are updated in
+ * place, many to a launch.
+ *
+ * State in 32 bits (state_dtype F32): exp_avg holds m, exp_avg_sq v.
+ * State in 8 bits (E4M3): exp_avg holds m and exp_avg_sq holds sqrt(v), each
+ * over its block's scale: FFF_ADAMW_BLOCK consecutive elements of a tensor
+ * (the last block may be short) share the two float32 of scale[block][2],
+ * (m, sqrt(v)), each max(largest size in the block / 448, 2^-126).  p uses
+ * the new moments before they are rounded.  A sqrt(v) above zero never
+ * becomes zero.  All-zero bytes are the state before the first step.
+ *
+ * With `stochastic`, 8-bit states, and bf16 weights that have no master, are
+ * rounded up or down with the probabilities that keep their mean, from the
+ * numbers hash(seed, tensor's place in the list, element): give every step
+ * another seed.  To nearest, a second moment whose decay moves it by less
+ * than half of an 8-bit step would never move, and a weight would lose
+ * updates below half of its bf16 step.
+ */
+#define FFF_ADAMW_BLOCK 128
+
+typedef struct fff_adamw_tensor {
+    void *param;          /* [n] param_dtype */
+    float *master;        /* [n] float32 master of a bf16 param, which then is its
+                             copy; or NULL */
+    const void *grad;     /* [n] grad_dtype */
+    void *exp_avg;        /* [n] state_dtype */
+    void *exp_avg_sq;     /* [n] state_dtype */
+    float *scale;         /* [ceil(n / 128)][2], 8-byte aligned; E4M3 only */
+    int64_t n;            /* elements, 0 <= n <= 2^34 (0: skipped) */
+    int32_t param_dtype;  /* F32 or BF16 */
+    int32_t grad_dtype;   /* F32 or BF16 */
+    double lr_scale;      /* the tensor's share of lr */
+    double weight_decay;
+} fff_adamw_tensor_t;
+
+typedef struct fff_adamw_config {
+    double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps >= 0 */
+    int64_t step;                  /* this step's number, from 1 */
+    int32_t state_dtype;           /* F32 or E4M3, for all tensors */
+    int32_t stochastic;            /* nonzero: as above */
+    uint64_t seed;
+    const float *grad_scale;       /* device: factor on every gradient (fff_grad_norm's
+                                      out + 1), or NULL for 1.  If it is NaN the step
+                                      leaves every tensor as it was */
+} fff_adamw_config_t;
+
+/* `tensors` is a host array, read before the call returns (a captured call
+ * keeps its pointers and numbers, `step` and `lr` among them). */
+fff_status_t fff_adamw_step(const fff_adamw_config_t *config, const fff_adamw_tensor_t *tensors,
+                            int64_t count, hipStream_t stream);
+
+/*
+ * The norm of all gradients together, in the tensors' order (only grad,
+ * grad_dtype and n are used): out[0] = sqrt(sum of squares), out[1] =
+ * min(1, max_norm / (norm + 1e-6)), or NaN where the norm is not finite in
+ * 32 bits.  Squares are summed in 64 bits in a fixed order.  max_norm > 0
+ * (infinity: no clipping).  out: device, 2 floats.
+ */
+fff_status_t fff_grad_norm_workspace_size(const fff_adamw_tensor_t *tensors, int64_t count,
+                                          size_t *bytes);
+fff_status_t fff_grad_norm(const fff_adamw_tensor_t *tensors, int64_t count, double max_norm,
+                           float *out, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream);
 
 /* Static, human-readable text for a status code. */
 const char *fff_status_string(fff_status_t status);

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(_PKG, "libfff.so")
@@ -18,6 +18,7 @@ LIBRARY = os.path.join(_PKG, "libfff.so")
 # fff_dtype_t
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_E4M3 = 2
 # fff_status_t
 SUCCESS = 0
 ERROR_INVALID_VALUE = 1
@@ -65,6 +66,31 @@ class Pruning(ctypes.Structure):
                 ("col_tiles", ctypes.c_int32)]
 
 
+class NormShape(ctypes.Structure):
+    """fff_norm_shape_t."""
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """fff_adamw_tensor_t."""
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("lr_scale", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class AdamwConfig(ctypes.Structure):
+    """fff_adamw_config_t."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64),
+                ("state_dtype", ctypes.c_int32), ("stochastic", ctypes.c_int32),
+                ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p)]
+
+
 class FFFError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -76,7 +102,10 @@ EXPORTS = ("fff_plan_default", "fff_plan_resolve", "fff_workspace_size", "fff_fo
            "fff_status_string", "fff_algo_name",
            "fff_prune_table_size", "fff_prune_prepare", "fff_forward_pruned",
            "fff_backward_workspace_size", "fff_backward", "fff_forward_static",
-           "fff_backward_pruned_workspace_size", "fff_backward_pruned")
+           "fff_backward_pruned_workspace_size", "fff_backward_pruned",
+           "fff_rms_norm", "fff_rms_norm_backward_workspace_size", "fff_rms_norm_backward",
+           "fff_adamw_step", "fff_grad_norm_workspace_size", "fff_grad_norm")
+ADAMW_BLOCK = 128  # FFF_ADAMW_BLOCK: elements per scale of an 8-bit state
 STATIC_SCRATCH_BYTES = 32 << 20  # FFF_STATIC_SCRATCH_BYTES
 
 _lib: Optional[ctypes.CDLL] = None
@@ -115,6 +144,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                         vp, sz, vp]
     lib.fff_forward_static.argtypes = [SP, PP, vp, vp, vp, vp, vp, vp, vp, vp,
                                        ctypes.POINTER(StageEvents)]
+    NP, TP = ctypes.POINTER(NormShape), ctypes.POINTER(AdamwTensor)
+    lib.fff_rms_norm.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.fff_rms_norm_backward_workspace_size.argtypes = [NP, ctypes.POINTER(sz)]
+    lib.fff_rms_norm_backward.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fff_adamw_step.argtypes = [ctypes.POINTER(AdamwConfig), TP, ctypes.c_int64, vp]
+    lib.fff_grad_norm_workspace_size.argtypes = [TP, ctypes.c_int64, ctypes.POINTER(sz)]
+    lib.fff_grad_norm.argtypes = [TP, ctypes.c_int64, ctypes.c_double, vp, vp, sz, vp]
     lib.fff_status_string.argtypes = [ctypes.c_int]
     lib.fff_status_string.restype = ctypes.c_char_p
     lib.fff_algo_name.argtypes = [ctypes.c_int32]
@@ -123,7 +159,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "fff_route", "fff_project", "fff_project_workspace_size", "fff_project_ws",
                  "fff_prune_table_size", "fff_prune_prepare",
                  "fff_forward_pruned", "fff_backward_workspace_size", "fff_backward",
-                 "fff_forward_static"):
+                 "fff_forward_static", "fff_rms_norm", "fff_rms_norm_backward_workspace_size",
+                 "fff_rms_norm_backward", "fff_adamw_step", "fff_grad_norm_workspace_size",
+                 "fff_grad_norm"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -546,3 +584,322 @@ def _backward(x, W_node, b_node, V_node, W_out, dy, pruning, algo, split_level, 
     if st != SUCCESS:
         raise FFFError(st, what)
     return g
+
+
+# ---- around the layer: norm and optimiser ----
+
+class RmsNorm(NamedTuple):
+    """rms_norm's outputs; None where not asked for or not there."""
+    y: object             # [T,d], the layer's dtype or float8_e4m3fn
+    residual_out: object  # [T,d] x + residual
+    rstd: object          # [T] float32, for the backward pass
+    scale: object         # [T, groups] float32 beside an 8-bit y
+
+
+class RmsNormGrad(NamedTuple):
+    dz: object       # [T,d] of the residual stream's dtype: the gradient of x and of the residual
+    dx: object       # [T,d] the same in the layer's dtype (dz itself where the dtypes agree)
+    dweight: object  # [d] float32
+
+
+def _here(device, stream):
+    """The handle of the stream to launch on: `stream`, or the current one.
+    The library launches on the current device, so tensors must be there."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, which is not the current device")
+    return torch.cuda.current_stream().cuda_stream if stream is None else int(stream.cuda_stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream it is used on."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _tensor(t, shape, dtype, device, what):
+    """The pointer of a tensor that must have this shape, dtype and device
+    and be contiguous; 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset: float = 0.0,
+             out_dtype=None, group: int = 0, y=None, scale=None, residual_out=None, rstd=None,
+             want_rstd: bool = False, stream=None) -> RmsNorm:
+    """fff_rms_norm: y = z * rstd * (weight + weight_offset) with
+    z = x + residual, over rows [T,d].
+
+    The layer's dtype is the weight's, else x's; the residual (and
+    residual_out) may be float32 beside a bf16 layer, and so may x where
+    there is no residual.  ``out_dtype`` torch.float8_e4m3fn (or a ``y`` of
+    that dtype) gives y in 8 bits with a scale per row, or per ``group`` = 32,
+    64 or 128 columns.  ``residual_out`` may be ``residual`` itself."""
+    torch = _torch()
+    T, d = _dims(x, 2, "x [T,d]")
+    shape, dev = x.shape, x.device
+    ty = weight.dtype if weight is not None else x.dtype
+    code = _dtype_code(weight if weight is not None else x)
+    if residual is None:
+        stream_ty, stream_code = x.dtype, _dtype_code(x)
+    else:
+        stream_ty, stream_code = residual.dtype, _dtype_code(residual)
+        if x.dtype != ty:
+            raise ValueError(f"x must be {ty} beside a residual, got {x.dtype}")
+    out_ty = y.dtype if y is not None else (out_dtype or ty)
+    if out_dtype is not None and out_ty != out_dtype:
+        raise ValueError(f"y must be {out_dtype}, got {out_ty}")
+    e4m3 = out_ty == torch.float8_e4m3fn
+    if not e4m3 and out_ty != ty:
+        raise ValueError(f"y must be {ty} or torch.float8_e4m3fn, got {out_ty}")
+    px = _tensor(x, shape, x.dtype, dev, "x")
+    pr = _tensor(residual, shape, stream_ty, dev, "residual")
+    pw = _tensor(weight, (d,), ty, dev, "weight [d]")
+    handle = _here(dev, stream)
+    if residual is None and stream_ty != ty:  # x is the stream itself
+        px, pr = 0, px
+    if y is None:
+        y = _empty(shape, out_ty, dev, stream)
+    py = _tensor(y, shape, out_ty, dev, "y")
+    if residual is not None and residual_out is None:
+        residual_out = _empty(shape, stream_ty, dev, stream)
+    pz = _tensor(residual_out, shape, stream_ty, dev, "residual_out")
+    if rstd is None and want_rstd:
+        rstd = _empty((T,), torch.float32, dev, stream)
+    ps = 0
+    if e4m3:
+        groups = (T, -(-d // group) if group > 0 else 1)
+        if scale is None:
+            scale = _empty(groups, torch.float32, dev, stream)
+        ps = _tensor(scale, groups, torch.float32, dev, "scale [T, groups]")
+    elif scale is not None:
+        raise ValueError("scale is for a y of torch.float8_e4m3fn")
+    st = load_library().fff_rms_norm(
+        NormShape(T, d, code, stream_code, DTYPE_E4M3 if e4m3 else code, group, eps, weight_offset),
+        px, pr, pw, py, ps, pz, _tensor(rstd, (T,), torch.float32, dev, "rstd [T]"), handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_rms_norm")
+    return RmsNorm(y, residual_out, rstd, scale)
+
+
+def rms_norm_backward_workspace_size(T: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    st = load_library().fff_rms_norm_backward_workspace_size(
+        NormShape(T, d, DTYPE_F32, DTYPE_F32, DTYPE_F32, 0, 0.0, 0.0), ctypes.byref(n))
+    if st != SUCCESS:
+        raise FFFError(st, "fff_rms_norm_backward_workspace_size")
+    return n.value
+
+
+def rms_norm_backward(dy, z, weight, rstd, *, dresidual=None, weight_offset: float = 0.0, dz=None,
+                      dx=None, dweight=None, want_dweight: bool = True, workspace=None,
+                      stream=None) -> RmsNormGrad:
+    """fff_rms_norm_backward: the gradients of rms_norm's inputs.  ``z`` is
+    what it normalised (its residual_out, or x), ``rstd`` its rstd and
+    ``dresidual`` the gradient that reaches residual_out.  Where z is float32
+    beside a bf16 layer, dx is dz once more in bf16."""
+    torch = _torch()
+    T, d = _dims(dy, 2, "dy [T,d]")
+    shape, dev = dy.shape, dy.device
+    ty, code = dy.dtype, _dtype_code(dy)
+    zty, zcode = z.dtype, _dtype_code(z)
+    f32 = torch.float32
+    pdy = _tensor(dy, shape, ty, dev, "dy")
+    pz = _tensor(z, shape, zty, dev, "z")
+    pw = _tensor(weight, (d,), ty, dev, "weight [d]")
+    pr = _tensor(rstd, (T,), f32, dev, "rstd [T]")
+    pe = _tensor(dresidual, shape, zty, dev, "dresidual")
+    handle = _here(dev, stream)
+    if dz is None:
+        dz = _empty(shape, zty, dev, stream)
+    if dx is None and zty != ty:
+        dx = _empty(shape, ty, dev, stream)
+    if dweight is None and want_dweight:
+        dweight = _empty((d,), f32, dev, stream)
+    need = rms_norm_backward_workspace_size(T, d) if dweight is not None else 0
+    if workspace is None and need:
+        workspace = _empty((need,), torch.uint8, dev, stream)
+    if workspace is not None:
+        _check([workspace], torch.uint8, dev)
+    st = load_library().fff_rms_norm_backward(
+        NormShape(T, d, code, zcode, code, 0, 0.0, weight_offset), pdy, pz, pw, pr, pe,
+        _tensor(dz, shape, zty, dev, "dz"), _tensor(dx, shape, ty, dev, "dx"),
+        _tensor(dweight, (d,), f32, dev, "dweight [d]"),
+        workspace.data_ptr() if workspace is not None else 0,
+        workspace.numel() if workspace is not None else 0, handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_rms_norm_backward")
+    return RmsNormGrad(dz, dz if dx is None else dx, dweight)
+
+
+class TensorTable:
+    """The tensors of an optimiser, laid out for the library: made once by
+    adamw_table or grad_table, used at every step.  It keeps the tensors
+    alive; they are updated in place and must keep their storage (make
+    another table where a tensor is replaced)."""
+
+    def __init__(self, entries, device, state_code, keep):
+        self.entries = entries        # array of AdamwTensor
+        self.count = len(entries)
+        self.device = device
+        self.state_code = state_code  # None: gradients only
+        self.keep = keep
+        n = ctypes.c_size_t()
+        st = load_library().fff_grad_norm_workspace_size(entries, self.count, ctypes.byref(n))
+        if st != SUCCESS:
+            raise FFFError(st, "fff_grad_norm_workspace_size")
+        self.norm_workspace = n.value
+
+
+def _flat(t, n, dtypes, device, what):
+    """The pointer of a contiguous tensor of n elements of one of `dtypes`."""
+    if t.numel() != n:
+        raise ValueError(f"{what} must have {n} elements, got {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and on {device}")
+    if device.type != "cuda":
+        raise ValueError(f"{what} must be on a GPU, not {device}")
+    return t.data_ptr()
+
+
+def _listed(values, n, what):
+    values = list(values) if isinstance(values, (list, tuple)) else [values] * n
+    if len(values) != n:
+        raise ValueError(f"{what} must have one entry for each of {n} tensors, got {len(values)}")
+    return values
+
+
+def grad_table(grads) -> TensorTable:
+    """A table of gradients alone, for grad_norm."""
+    torch = _torch()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    entries = (AdamwTensor * len(grads))()
+    for i, (e, g) in enumerate(zip(entries, grads)):
+        e.grad = _flat(g, g.numel(), (torch.float32, torch.bfloat16), grads[0].device, f"grads[{i}]")
+        e.n, e.grad_dtype = g.numel(), _dtype_code(g)
+    return TensorTable(entries, grads[0].device, None, grads)
+
+
+def adamw_state(params, bits: int = 32):
+    """The state before the first step, as adamw_table takes it: lists
+    (exp_avg, exp_avg_sq, scales), float32, or for ``bits`` = 8 float8_e4m3fn
+    with scales [blocks, 2] (else None)."""
+    torch = _torch()
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+    if bits == 32:
+        make = lambda p: torch.zeros(p.shape, dtype=torch.float32, device=p.device)  # noqa: E731
+        return [make(p) for p in params], [make(p) for p in params], None
+    make = lambda p: torch.zeros(p.shape, dtype=torch.uint8,  # noqa: E731
+                                 device=p.device).view(torch.float8_e4m3fn)
+    scales = [torch.zeros(-(-p.numel() // ADAMW_BLOCK), 2, dtype=torch.float32, device=p.device)
+              for p in params]
+    return [make(p) for p in params], [make(p) for p in params], scales
+
+
+def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None,
+                weight_decay=0.0, lr_scale=1.0) -> TensorTable:
+    """The tensors of an AdamW step: float32 or bf16 params and grads, states
+    of one dtype (float32, or float8_e4m3fn with ``scales``; adamw_state makes
+    them).  ``masters``: float32 masters of bf16 params (None, or a list with
+    None where a param has none).  ``weight_decay`` and ``lr_scale``: one
+    number, or one for each tensor."""
+    torch = _torch()
+    params = list(params)
+    n = len(params)
+    if n == 0:
+        raise ValueError("params must hold at least one tensor")
+    dev = params[0].device
+    f32, both = (torch.float32,), (torch.float32, torch.bfloat16)
+    lists = {"grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
+             "masters": masters, "scales": scales}
+    lists = {k: _listed(v, n, k) for k, v in lists.items()}
+    decays, shares = _listed(weight_decay, n, "weight_decay"), _listed(lr_scale, n, "lr_scale")
+    state = (lists["exp_avg"][0].dtype,)
+    e4m3 = state[0] == torch.float8_e4m3fn
+    if not e4m3 and state != f32:
+        raise ValueError(f"exp_avg must be torch.float32 or torch.float8_e4m3fn, got {state[0]}")
+    entries = (AdamwTensor * n)()
+    for i, (e, p) in enumerate(zip(entries, params)):
+        g, m, v, w, sc = (lists[k][i] for k in ("grads", "exp_avg", "exp_avg_sq", "masters", "scales"))
+        e.n = p.numel()
+        e.param = _flat(p, e.n, both, dev, f"params[{i}]")
+        e.grad = _flat(g, e.n, both, dev, f"grads[{i}]")
+        e.exp_avg = _flat(m, e.n, state, dev, f"exp_avg[{i}]")
+        e.exp_avg_sq = _flat(v, e.n, state, dev, f"exp_avg_sq[{i}]")
+        e.param_dtype, e.grad_dtype = _dtype_code(p), _dtype_code(g)
+        if w is not None:
+            if p.dtype != torch.bfloat16:
+                raise ValueError(f"masters[{i}] is for a bf16 param, params[{i}] is {p.dtype}")
+            e.master = _flat(w, e.n, f32, dev, f"masters[{i}]")
+        if e4m3 != (sc is not None):
+            raise ValueError("scales go with exp_avg of torch.float8_e4m3fn, and only with it")
+        if e4m3:
+            e.scale = _flat(sc, 2 * -(-e.n // ADAMW_BLOCK), f32, dev, f"scales[{i}]")
+        e.lr_scale, e.weight_decay = float(shares[i]), float(decays[i])
+    return TensorTable(entries, dev, DTYPE_E4M3 if e4m3 else DTYPE_F32, (params, lists))
+
+
+def adamw_step(table: TensorTable, *, lr: float, step: int, beta1: float = 0.9,
+               beta2: float = 0.999, eps: float = 1e-8, grad_scale=None, seed: Optional[int] = None,
+               stream=None) -> None:
+    """fff_adamw_step on a table's tensors, in place.  ``step`` counts from 1.
+    ``grad_scale``: a float32 device tensor of one element that multiplies
+    every gradient (grad_norm's second value), or None; if it holds NaN the
+    step changes nothing.  ``seed``: None rounds to nearest, a number (another
+    one at every step) rounds 8-bit states and bf16 params without a master
+    stochastically."""
+    torch = _torch()
+    if table.state_code is None:
+        raise ValueError("the table holds gradients only: make it with adamw_table")
+    ps = 0
+    if grad_scale is not None:
+        ps = _flat(grad_scale, 1, (torch.float32,), table.device, "grad_scale")
+    handle = _here(table.device, stream)
+    config = AdamwConfig(lr, beta1, beta2, eps, step, table.state_code, seed is not None,
+                         0 if seed is None else seed & 0xFFFFFFFFFFFFFFFF, ps)
+    st = load_library().fff_adamw_step(config, table.entries, table.count, handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_adamw_step")
+
+
+def grad_norm(grads, *, max_norm: float = float("inf"), out=None, workspace=None, stream=None):
+    """fff_grad_norm of a TensorTable or a list of tensors: a float32 device
+    tensor [2], the norm of all gradients together and the factor
+    min(1, max_norm / (norm + 1e-6)) (NaN where the norm is not finite) that
+    adamw_step takes as ``grad_scale`` (``out[1:]``)."""
+    torch = _torch()
+    table = grads if isinstance(grads, TensorTable) else grad_table(grads)
+    dev = table.device
+    handle = _here(dev, stream)
+    if out is None:
+        out = _empty((2,), torch.float32, dev, stream)
+    if workspace is None and table.norm_workspace:
+        workspace = _empty((table.norm_workspace,), torch.uint8, dev, stream)
+    if workspace is not None:
+        _check([workspace], torch.uint8, dev)
+    st = load_library().fff_grad_norm(
+        table.entries, table.count, max_norm, _tensor(out, (2,), torch.float32, dev, "out [2]"),
+        workspace.data_ptr() if workspace is not None else 0,
+        workspace.numel() if workspace is not None else 0, handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_grad_norm")
+    return out

@@ -1,0 +1,95 @@
+// Host-side launchers of the kernels around the layer: the norm with its
+// backward pass, the optimiser step and the gradient norm.  Each enqueues its
+// kernel(s) on `st` and returns hipGetLastError().  Arguments have been
+// validated by the C-ABI layer before any of these is called.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace fff {
+
+constexpr int kNormMaxWidth = 32768;  // sixteen wavefronts of four chunks of 8 columns per lane
+
+struct NormArgs {
+  int64_t T;
+  int d;
+  int group;          // e4m3: columns per scale, 0 = the row
+  bool bf16;          // layer type (x, weight, y)
+  bool stream_bf16;   // residual, residual_out
+  bool e4m3;          // y in 8 bits
+  float eps, weight_offset;
+  const void *x, *residual, *weight;
+  void* y;
+  float* scale;
+  void* residual_out;
+  float* rstd;
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t st);
+
+struct NormGradArgs {
+  int64_t T;
+  int d;
+  bool bf16, stream_bf16;
+  float weight_offset;
+  const void *dy, *z, *weight;
+  const float* rstd;
+  const void* dresidual;
+  void *dz, *dx;
+  float *dweight, *partial;
+};
+size_t rms_norm_backward_partials(int64_t T, int d);  // rows of d floats in the workspace
+hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st);
+
+// ---- optimiser ----
+
+constexpr int kStateBlock = 128;      // elements per scale of an 8-bit state
+constexpr int kAdamwChunk = 2048;     // elements per workgroup
+constexpr int kAdamwMaxTensors = 55;  // descriptors that fit a kernel's arguments (4 KB)
+
+struct AdamwEntry {
+  void* param;
+  float* master;
+  const void* grad;
+  void *exp_avg, *exp_avg_sq;
+  float* scale;
+  int64_t n;
+  uint32_t first;  // its first workgroup
+  uint32_t key;    // of its random numbers
+  float decay;     // 1 - lr weight_decay
+  float step;      // lr / (1 - beta1^t)
+};
+
+struct AdamwArgs {
+  float beta1, one_beta1, beta2, one_beta2, eps, root;  // root: 1 / sqrt(1 - beta2^t)
+  const float* grad_scale;
+  int count;
+  AdamwEntry e[kAdamwMaxTensors];
+};
+
+enum AdamwParam { kParamF32 = 0, kParamBf16 = 1, kParamMaster = 2 };
+
+hipError_t launch_adamw(const AdamwArgs& a, int blocks, int param, bool grad_bf16, bool state_e4m3,
+                        bool stochastic, hipStream_t st);
+
+constexpr int kNormChunk = 16384;   // gradient elements per workgroup
+constexpr int kNormMaxTensors = 160;
+
+struct GradEntry {
+  const void* grad;
+  int64_t n;         // elements; negative: bf16
+  uint32_t first;
+};
+
+struct GradNormArgs {
+  double* partial;   // one per workgroup
+  int count;
+  GradEntry e[kNormMaxTensors];
+};
+
+hipError_t launch_grad_squares(const GradNormArgs& a, int blocks, hipStream_t st);
+hipError_t launch_grad_norm_final(const double* partial, int64_t count, double max_norm, float* out,
+                                  hipStream_t st);
+
+}  // namespace fff
