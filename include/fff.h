@@ -426,9 +426,10 @@ fff_status_t fff_forward_static(const fff_shape_t *shape, const fff_plan_t *plan
  *
  * With out_dtype FFF_DTYPE_E4M3, y is held in 8 bits: for every row (group
  * 0) or every `group` columns of a row (32, 64 or 128; the last group may be
- * short) scale = max(largest |y| / 448, 2^-126) and the stored value is
- * y / scale to nearest.  A NaN in a group makes its scale NaN; a group whose
- * largest size is infinite has scale infinity.
+ * short) scale = max(largest |y| * (1/448), 2^-126) and the stored value is
+ * y * (1/scale) to nearest (both reciprocals rounded to 32 bits).  A NaN in
+ * a group makes its scale NaN; a group whose largest size is infinite has
+ * scale infinity.
  */
 typedef struct fff_norm_shape {
     int64_t T;             /* rows, 0 <= T < 2^31 */
@@ -492,8 +493,9 @@ fff_status_t fff_rms_norm_backward(const fff_norm_shape_t *shape, const void *dy
  * State in 8 bits (E4M3): exp_avg holds m and exp_avg_sq holds sqrt(v), each
  * over its block's scale: FFF_ADAMW_BLOCK consecutive elements of a tensor
  * (the last block may be short) share the two float32 of scale[block][2],
- * (m, sqrt(v)), each max(largest size in the block / 448, 2^-126).  p uses
- * the new moments before they are rounded.  A sqrt(v) above zero never
+ * (m, sqrt(v)), each max(largest size in the block * (1/448), 2^-126), and a
+ * code is the value * (1/scale) (both reciprocals rounded to 32 bits).  p
+ * uses the new moments before they are rounded.  A sqrt(v) above zero never
  * becomes zero.  All-zero bytes are the state before the first step.
  *
  * With `stochastic`, 8-bit states, and bf16 weights that have no master, are

@@ -18,12 +18,20 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
 // One tensor of the optimiser fits one launch.
 constexpr int64_t kMaxTensor = int64_t(1) << 34;
-static_assert(kMaxTensor / fff::kAdamwChunk <= kMaxBlocks, "a tensor fits a launch");
+static_assert(kMaxTensor / fff::kAdamwChunk <= kMaxBlocks &&
+                  (kMaxTensor >> 32) < (1 << (32 - fff::kFirstBits)) &&
+                  kMaxBlocks < (1 << fff::kFirstBits),
+              "a tensor fits a launch, and its descriptor the arguments");
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 size_t type_size(int32_t dtype) {
   return dtype == FFF_DTYPE_F32 ? 4 : dtype == FFF_DTYPE_BF16 ? 2 : 1;
+}
+
+// An address that gfx950 can have.
+bool in_space(const void* p) {
+  return reinterpret_cast<uintptr_t>(p) >> fff::kAddressBits == 0;
 }
 
 // A pointer that a tensor of this type can have.
@@ -193,7 +201,8 @@ fff_status_t fff_adamw_step(const fff_adamw_config_t* config, const fff_adamw_te
     if (t.n == 0) continue;
     if (!good(t.param, t.param_dtype) || !good_or_null(t.master, FFF_DTYPE_F32) ||
         !good(t.exp_avg, c.state_dtype) || !good(t.exp_avg_sq, c.state_dtype) ||
-        (e4m3 && !(t.scale && aligned(t.scale, 8))))
+        (e4m3 && !(t.scale && aligned(t.scale, 8))) || !in_space(t.param) || !in_space(t.master) ||
+        !in_space(t.grad) || !in_space(t.exp_avg) || !in_space(t.exp_avg_sq) || !in_space(t.scale))
       return FFF_ERROR_INVALID_VALUE;
     any[kind_of(t)] = true;
   }
@@ -224,15 +233,17 @@ fff_status_t fff_adamw_step(const fff_adamw_config_t* config, const fff_adamw_te
       const int64_t need = (t.n + fff::kAdamwChunk - 1) / fff::kAdamwChunk;
       if ((a.count == fff::kAdamwMaxTensors || blocks + need > kMaxBlocks) && flush() != hipSuccess)
         return FFF_ERROR_HIP;
-      fff::AdamwEntry& e = a.e[a.count++];
-      e.param = t.param;
-      e.master = t.master;
-      e.grad = t.grad;
-      e.exp_avg = t.exp_avg;
-      e.exp_avg_sq = t.exp_avg_sq;
-      e.scale = t.scale;
-      e.n = t.n;
-      e.first = static_cast<uint32_t>(blocks);
+      using E = fff::AdamwEntry;
+      a.first[a.count] = static_cast<uint32_t>(blocks) |
+                         static_cast<uint32_t>(t.n >> 32) << fff::kFirstBits;
+      E& e = a.e[a.count++];
+      e.set(E::kParam, t.param);
+      e.set(E::kMaster, t.master);
+      e.set(E::kGrad, t.grad);
+      e.set(E::kExpAvg, t.exp_avg);
+      e.set(E::kExpAvgSq, t.exp_avg_sq);
+      e.set(E::kScale, t.scale);
+      e.n_lo = static_cast<uint32_t>(t.n);
       e.key = random_key(c.seed, static_cast<uint32_t>(i));
       const double lr = c.lr * t.lr_scale;
       e.decay = static_cast<float>(1.0 - lr * t.weight_decay);
@@ -283,10 +294,10 @@ fff_status_t fff_grad_norm(const fff_adamw_tensor_t* tensors, int64_t count, dou
     const int64_t need = (t.n + fff::kNormChunk - 1) / fff::kNormChunk;
     if ((a.count == fff::kNormMaxTensors || blocks + need > kMaxBlocks) && flush() != hipSuccess)
       return FFF_ERROR_HIP;
+    a.first[a.count] = static_cast<uint32_t>(blocks);
     fff::GradEntry& e = a.e[a.count++];
     e.grad = t.grad;
     e.n = t.grad_dtype == FFF_DTYPE_BF16 ? -t.n : t.n;
-    e.first = static_cast<uint32_t>(blocks);
     blocks += need;
   }
   if (flush() != hipSuccess) return FFF_ERROR_HIP;

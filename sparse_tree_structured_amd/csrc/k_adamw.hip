@@ -27,18 +27,21 @@ namespace {
 constexpr int kThreads = 256;
 static_assert(kAdamwChunk == kThreads * 8 && kStateBlock == 16 * 8, "16 lanes hold a block");
 
-// The entry whose workgroups `block` is one of (first ascending, e[0].first = 0).
-template <typename Args>
-__device__ __forceinline__ int entry_of(const Args& a, uint32_t block) {
-  int lo = 0, hi = a.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.e[mid].first <= block)
-      lo = mid;
-    else
-      hi = mid;
+constexpr uint32_t kFirstMask = (1u << kFirstBits) - 1;
+
+// The entry whose workgroups `block` is one of: the last whose first
+// workgroup (the low 24 bits of first[], ascending from 0) is not past it.
+// Each lane looks at its own entries, so the search costs one load and not a
+// chain of them.
+template <int MOST>
+__device__ __forceinline__ int entry_of(const uint32_t (&first)[MOST], int count, uint32_t block) {
+  int at = -1;
+#pragma unroll
+  for (int base = 0; base < MOST; base += kWave) {
+    const int i = base + (threadIdx.x & (kWave - 1));
+    at += __popcll(__ballot(i < count && (first[i < MOST ? i : 0] & kFirstMask) <= block));
   }
-  return lo;
+  return at;
 }
 
 // MurmurHash3's 32-bit finaliser (Appleby; public domain).
@@ -50,43 +53,24 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-// |t| <= 448 to an e4m3 value, down or up by the uniform u = bits / 2^16:
-// floor(|t| / step + u) step, step = 2^(exponent - 3), at least 2^-9.
-__device__ __forceinline__ float stochastic_e4m3(float t, uint32_t bits16) {
+// Eight elements from i0 on; n of them (8 where FULL) belong to the tensor.
+template <int PARAM, typename G, bool E4M3, bool STOCHASTIC, bool FULL>
+__device__ __forceinline__ void adamw_eight(const AdamwArgs& a, const AdamwEntry& t, int64_t size,
+                                            int64_t i0) {
 #pragma clang fp contract(off)
-  const float a = fabsf(t);
-  const uint32_t e = umax(__float_as_uint(a) >> 23, 121u);
-  const float up = __uint_as_float((257u - e) << 23);
-  const float down = __uint_as_float((e - 3u) << 23);
-  const float k = floorf(a * up + static_cast<float>(bits16) * (1.0f / 65536.0f));
-  return copysignf(fminf(k * down, kE4m3Max), t);
-}
-
-// 32 bits to bf16, up in size with the probability that the lost bits name.
-__device__ __forceinline__ float stochastic_bf16(float v, uint32_t bits16) {
-  const uint32_t b = __float_as_uint(v);
-  if (size_bits(v) > 0x7f800000u) return v;  // NaN: the sum below could leave the format
-  return __uint_as_float((b + bits16) & 0xffff0000u);
-}
-
-template <int PARAM, typename G, bool E4M3, bool STOCHASTIC>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
-#pragma clang fp contract(off)
-  const AdamwEntry& t = a.e[entry_of(a, blockIdx.x)];
-  const int64_t i0 = int64_t(blockIdx.x - t.first) * kAdamwChunk + threadIdx.x * 8;
-  const int n = t.n - i0 >= 8 ? 8 : static_cast<int>(t.n - i0 > 0 ? t.n - i0 : 0);
+  const int n = FULL || size - i0 >= 8 ? 8 : static_cast<int>(size - i0 > 0 ? size - i0 : 0);
   using P = typename std::conditional<PARAM == kParamBf16, uint16_t, float>::type;
-  P* const p = (PARAM == kParamMaster ? reinterpret_cast<P*>(t.master) : static_cast<P*>(t.param)) + i0;
+  P* const p = t.get<P>(PARAM == kParamMaster ? t.kMaster : t.kParam) + i0;
   Eight<P> pr;
   Eight<G> gr;
   load_eight(pr, static_cast<const P*>(p), n);
-  load_eight(gr, static_cast<const G*>(t.grad) + i0, n);
+  load_eight(gr, t.get<const G>(t.kGrad) + i0, n);
   float m[8], r[8];
-  uint8_t* const mq = static_cast<uint8_t*>(t.exp_avg) + i0;
-  uint8_t* const rq = static_cast<uint8_t*>(t.exp_avg_sq) + i0;
-  float* const mf = static_cast<float*>(t.exp_avg) + i0;
-  float* const vf = static_cast<float*>(t.exp_avg_sq) + i0;
-  f32x2_t* const scale = reinterpret_cast<f32x2_t*>(t.scale) + i0 / kStateBlock;
+  uint8_t* const mq = t.get<uint8_t>(t.kExpAvg) + i0;
+  uint8_t* const rq = t.get<uint8_t>(t.kExpAvgSq) + i0;
+  float* const mf = t.get<float>(t.kExpAvg) + i0;
+  float* const vf = t.get<float>(t.kExpAvgSq) + i0;
+  f32x2_t* const scale = t.get<f32x2_t>(t.kScale) + i0 / kStateBlock;
   if constexpr (E4M3) {
     EightE4m3 qm, qr;
     qm.load(mq, n);
@@ -123,56 +107,84 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
     const float root = sqrtf(v);
     w[i] = pr.get(i) * t.decay - t.step * (m[i] / (root * a.root + a.eps));
     r[i] = E4M3 ? root : v;
-    if (E4M3 && i < n) {
+    if (E4M3) {
       top_m = umax(top_m, size_bits(m[i]));
-      top_r = umax(top_r, size_bits(root));
+      top_r = umax(top_r, __float_as_uint(root));  // root >= 0, or NaN
     }
   }
   if (gs != gs) return;  // the gradient's norm was not finite: no step
-  uint32_t h[8];
+  uint32_t h[8], rnd[8];
   if constexpr (STOCHASTIC) {
     const uint32_t base = t.key ^ (static_cast<uint32_t>(i0 >> 32) * 0x9E3779B9u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = mix32((static_cast<uint32_t>(i0) + i) ^ base);
   }
-  if constexpr (PARAM == kParamMaster) {
-    store_eight(static_cast<uint16_t*>(t.param) + i0, n, w);
-  } else if constexpr (PARAM == kParamBf16 && STOCHASTIC) {
-    float v[8];
+  if constexpr (PARAM == kParamMaster) store_eight(t.get<uint16_t>(t.kParam) + i0, n, w);
+  if constexpr (PARAM == kParamBf16 && STOCHASTIC) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = stochastic_bf16(w[i], mix32(h[i] ^ 0x9E3779B9u) & 0xffffu);
-    store_eight(p, n, v);
+    for (int i = 0; i < 8; ++i) rnd[i] = mix32(h[i] ^ 0x9E3779B9u) << 16;
+    store_packed(p, n, pack_bf16_stochastic(w, rnd));
+  } else {
+    store_eight(p, n, w);
   }
-  if constexpr (!(PARAM == kParamBf16 && STOCHASTIC)) store_eight(p, n, w);
   if constexpr (!E4M3) {
     store_eight(mf, n, m);
     store_eight(vf, n, r);
-  } else {
-    const float sm = e4m3_scale(group_max<16>(top_m));
-    const float sr = e4m3_scale(group_max<16>(top_r));
-    const float im = 1.0f / sm, ir = 1.0f / sr;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float tm = m[i] * im, tr = r[i] * ir;
-      m[i] = STOCHASTIC ? stochastic_e4m3(tm, h[i] & 0xffffu) : tm;
-      const float q = STOCHASTIC ? stochastic_e4m3(tr, h[i] >> 16) : tr;
-      r[i] = tr > 0.0f ? fmaxf(q, 0.001953125f) : q;
-    }
-    if (n > 0) {
-      store_e4m3(mq, n, m);
-      store_e4m3(rq, n, r);
-      if (threadIdx.x % 16 == 0) *scale = f32x2_t{sm, sr};
-    }
+    return;
   }
+  // Lanes past the tensor's end hold zeros, which no maximum sees.
+  const float sm = e4m3_scale(group_max<16>(top_m));
+  const float sr = e4m3_scale(group_max<16>(top_r));
+  const float im = 1.0f / sm, ir = 1.0f / sr;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m[i] *= im;
+    r[i] *= ir;
+    // at least the smallest code, which every rounding of it keeps
+    r[i] = r[i] > 0.0f ? fmaxf(r[i], 0.001953125f) : r[i];
+  }
+  u32x2_t qm, qr;
+  if constexpr (STOCHASTIC) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rnd[i] = h[i] << 16;
+    qm = pack_e4m3_stochastic(m, rnd);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rnd[i] = h[i] & 0xffff0000u;
+    qr = pack_e4m3_stochastic(r, rnd);
+  } else {
+    qm = pack_e4m3(m);
+    qr = pack_e4m3(r);
+  }
+  if (n > 0) {
+    store_packed(mq, n, qm);
+    store_packed(rq, n, qr);
+    if (threadIdx.x % 16 == 0) *scale = f32x2_t{sm, sr};
+  }
+}
+
+// One chunk of one tensor.  A chunk inside its tensor runs without any tests
+// for the tensor's end.
+template <int PARAM, typename G, bool E4M3, bool STOCHASTIC>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
+  const int at = entry_of(a.first, a.count, blockIdx.x);
+  const AdamwEntry& t = a.e[at];
+  const uint32_t first = a.first[at];
+  const int64_t size = int64_t(first >> kFirstBits) << 32 | t.n_lo;
+  const int64_t begin = int64_t(blockIdx.x - (first & kFirstMask)) * kAdamwChunk;
+  if (size - begin >= kAdamwChunk)
+    adamw_eight<PARAM, G, E4M3, STOCHASTIC, true>(a, t, size, begin + threadIdx.x * 8);
+  else
+    adamw_eight<PARAM, G, E4M3, STOCHASTIC, false>(a, t, size, begin + threadIdx.x * 8);
 }
 
 // Sum of squares of one chunk of one tensor, in 64 bits: neither a large
 // gradient nor the number of elements costs the sum anything.
 __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) {
-  const GradEntry& t = a.e[entry_of(a, blockIdx.x)];
+  const int at = entry_of(a.first, a.count, blockIdx.x);
+  const GradEntry& t = a.e[at];
   const bool bf16 = t.n < 0;
   const int64_t n = bf16 ? -t.n : t.n;
-  const int64_t begin = int64_t(blockIdx.x - t.first) * kNormChunk;
+  const int64_t begin = int64_t(blockIdx.x - a.first[at]) * kNormChunk;
   double s = 0.0;
 #pragma unroll 4
   for (int k = 0; k < kNormChunk / (kThreads * 8); ++k) {

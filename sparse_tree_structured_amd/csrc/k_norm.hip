@@ -134,7 +134,7 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[c][i] *= inv;
         if (col < a.d) {
-          store_e4m3(y + row + col, a.d - col, z[c]);
+          store_packed(y + row + col, a.d - col, pack_e4m3(z[c]));
           if (a.group == 0) {
             if (col == 0) a.scale[t] = scale;
           } else if (col % a.group == 0) {
@@ -220,23 +220,36 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_backward_kernel
   }
 }
 
-// dw[j] = sum over the partials in their order: 64 columns per workgroup,
-// sixteen slices of the partials, joined in LDS.
-__global__ __launch_bounds__(1024) void rms_norm_dweight_kernel(const float* partial, int count,
-                                                                int d, float* dw) {
-  __shared__ float lds[16][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63);
-  const int slice = threadIdx.x >> 6;
+// dw[j] = sum over the partials in a fixed order: 16 columns (one 64-byte
+// piece of every partial) per workgroup, 64 slices of the partials, sixteen
+// loads in flight per lane, the slices joined in LDS.
+constexpr int kSumCols = 16, kSumSlices = 64;
+
+__global__ __launch_bounds__(kSumCols * kSumSlices) void rms_norm_dweight_kernel(
+    const float* partial, int count, int d, float* dw) {
+  __shared__ float lds[kSumSlices][kSumCols + 1];
+  const int lane = threadIdx.x % kSumCols;
+  const int col = blockIdx.x * kSumCols + lane;
+  const int slice = threadIdx.x / kSumCols;
   float s = 0.0f;
-  if (col < d)
-    for (int i = slice; i < count; i += 16) s += partial[size_t(i) * d + col];
-  lds[slice][threadIdx.x & 63] = s;
-  __syncthreads();
-  if (slice == 0 && col < d) {
-    float v = 0.0f;
+  if (col < d) {
+    const float* p = partial + col;
+    for (int i = slice; i < count; i += 16 * kSumSlices) {
+      float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += lds[i][threadIdx.x & 63];
-    dw[col] = v;
+      for (int k = 0; k < 16; ++k)
+        v[k] = i + k * kSumSlices < count ? p[size_t(i + k * kSumSlices) * d] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s += v[k];
+    }
+  }
+  lds[slice][lane] = s;
+  __syncthreads();
+  if (threadIdx.x < kSumCols && col < d) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSumSlices; ++i) s += lds[i][threadIdx.x];
+    dw[col] = s;
   }
 }
 
@@ -317,8 +330,8 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st) {
   else
     e = run_bwd<float, float>(a, p, st);
   if (e != hipSuccess || !a.dweight) return e;
-  rms_norm_dweight_kernel<<<(a.d + 63) / 64, 1024, 0, st>>>(a.partial, p.grid * p.rows, a.d,
-                                                           a.dweight);
+  rms_norm_dweight_kernel<<<(a.d + kSumCols - 1) / kSumCols, kSumCols * kSumSlices, 0, st>>>(
+      a.partial, a.T == 0 ? 0 : p.grid * p.rows, a.d, a.dweight);
   return hipGetLastError();
 }
 

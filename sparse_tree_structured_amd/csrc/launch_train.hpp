@@ -46,27 +46,41 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st);
 
 constexpr int kStateBlock = 128;      // elements per scale of an 8-bit state
 constexpr int kAdamwChunk = 2048;     // elements per workgroup
-constexpr int kAdamwMaxTensors = 55;  // descriptors that fit a kernel's arguments (4 KB)
+constexpr int kAdamwMaxTensors = 72;  // descriptors that fit a kernel's arguments (4 KB)
 
+// One tensor.  Every launch has a tail of a few microseconds in which the
+// last workgroups compute and nothing loads, so as many tensors as possible
+// go into one: addresses are kept in gfx950's 48 bits.
 struct AdamwEntry {
-  void* param;
-  float* master;
-  const void* grad;
-  void *exp_avg, *exp_avg_sq;
-  float* scale;
-  int64_t n;
-  uint32_t first;  // its first workgroup
-  uint32_t key;    // of its random numbers
-  float decay;     // 1 - lr weight_decay
-  float step;      // lr / (1 - beta1^t)
+  enum { kParam, kMaster, kGrad, kExpAvg, kExpAvgSq, kScale, kPointers };
+  uint32_t lo[kPointers];
+  uint16_t hi[kPointers];
+  uint32_t n_lo;  // elements: low half (the high bits are in AdamwArgs::first)
+  float decay;    // 1 - lr weight_decay
+  float step;     // lr / (1 - beta1^t)
+  uint32_t key;   // of its random numbers
+
+  void set(int which, const void* p) {
+    lo[which] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+    hi[which] = static_cast<uint16_t>(reinterpret_cast<uintptr_t>(p) >> 32);
+  }
+  template <typename T> __host__ __device__ T* get(int which) const {
+    return reinterpret_cast<T*>(static_cast<uintptr_t>(lo[which]) |
+                                static_cast<uintptr_t>(hi[which]) << 32);
+  }
 };
+constexpr int kAddressBits = 48;
+constexpr int kFirstBits = 24;  // workgroups of a launch: below 2^24
 
 struct AdamwArgs {
   float beta1, one_beta1, beta2, one_beta2, eps, root;  // root: 1 / sqrt(1 - beta2^t)
   const float* grad_scale;
   int count;
+  // Each tensor's first workgroup (24 bits) and, above it, its n >> 32.
+  uint32_t first[kAdamwMaxTensors];
   AdamwEntry e[kAdamwMaxTensors];
 };
+static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
 
 enum AdamwParam { kParamF32 = 0, kParamBf16 = 1, kParamMaster = 2 };
 
@@ -74,19 +88,20 @@ hipError_t launch_adamw(const AdamwArgs& a, int blocks, int param, bool grad_bf1
                         bool stochastic, hipStream_t st);
 
 constexpr int kNormChunk = 16384;   // gradient elements per workgroup
-constexpr int kNormMaxTensors = 160;
+constexpr int kNormMaxTensors = 192;
 
 struct GradEntry {
   const void* grad;
   int64_t n;         // elements; negative: bf16
-  uint32_t first;
 };
 
 struct GradNormArgs {
   double* partial;   // one per workgroup
   int count;
+  uint32_t first[kNormMaxTensors];
   GradEntry e[kNormMaxTensors];
 };
+static_assert(sizeof(GradNormArgs) <= 4096, "kernel arguments");
 
 hipError_t launch_grad_squares(const GradNormArgs& a, int blocks, hipStream_t st);
 hipError_t launch_grad_norm_final(const double* partial, int64_t count, double max_norm, float* out,

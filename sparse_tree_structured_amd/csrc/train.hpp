@@ -101,14 +101,56 @@ __device__ __forceinline__ u32x2_t pack_e4m3(const float (&v)[8]) {
   return r;
 }
 
-__device__ __forceinline__ void store_e4m3(uint8_t* p, int n, const float (&v)[8]) {
-  const u32x2_t r = pack_e4m3(v);
+// The same down or up with the probabilities that keep the mean:
+// floor(|v| / step + u) step, step an e4m3 step at |v| (2^-9 below 2^-6),
+// u = the high 16 bits of rnd over 2^16 (its low 16 bits must be 0).  This is
+// what gfx950's v_cvt_sr_fp8_f32 does, exact for normal and subnormal results
+// (compared with the formula on four million values); it replaces eleven
+// operations an element.  A |v| that its scaling left a few units above 448
+// stays at 448: the carry into the next step needs more than 15 units.
+__device__ __forceinline__ u32x2_t pack_e4m3_stochastic(const float (&v)[8], const uint32_t (&rnd)[8]) {
+  u32x2_t r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int w = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i], rnd[4 * i], 0, 0);
+    w = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i + 1], rnd[4 * i + 1], w, 1);
+    w = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i + 2], rnd[4 * i + 2], w, 2);
+    r[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i + 3], rnd[4 * i + 3], w, 3);
+  }
+  return r;
+}
+
+// 32 bits to bf16 in the same way (v_cvt_sr_bf16_f32; NaN stays NaN).
+__device__ __forceinline__ u32x4_t pack_bf16_stochastic(const float (&v)[8], const uint32_t (&rnd)[8]) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bf16x2_t w = {};
+    w = __builtin_amdgcn_cvt_sr_bf16_f32(w, v[2 * i], rnd[2 * i], false);
+    w = __builtin_amdgcn_cvt_sr_bf16_f32(w, v[2 * i + 1], rnd[2 * i + 1], true);
+    r[i] = __builtin_bit_cast(uint32_t, w);
+  }
+  return r;
+}
+
+// The first n of eight packed elements.
+__device__ __forceinline__ void store_packed(uint8_t* p, int n, u32x2_t r) {
   if (n >= 8) {
     *reinterpret_cast<u32x2_a1_t*>(p) = r;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = static_cast<uint8_t>(r[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+__device__ __forceinline__ void store_packed(uint16_t* p, int n, u32x4_t r) {
+  if (n >= 8) {
+    *reinterpret_cast<u32x4_a2_t*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = static_cast<uint16_t>(r[i >> 1] >> (16 * (i & 1)));
   }
 }
 
@@ -192,7 +234,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 
 // The scale of a group whose largest size has these bits (NaN stays NaN).
 __device__ __forceinline__ float e4m3_scale(uint32_t bits) {
-  const float s = __uint_as_float(bits) / kE4m3Max;
+  const float s = __uint_as_float(bits) * (1.0f / kE4m3Max);
   return s < kTinyScale ? kTinyScale : s;
 }
 

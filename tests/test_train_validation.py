@@ -128,7 +128,7 @@ def test_adamw_state_type(lib):
 @pytest.mark.parametrize("over,code", [
     (dict(param=None), 1), (dict(grad=None), 1), (dict(exp_avg=None), 1), (dict(exp_avg_sq=None), 1),
     (dict(param=FAKE + 2), 1), (dict(grad=ODD), 1), (dict(exp_avg=FAKE + 2), 1), (dict(n=-1), 1),
-    (dict(n=(1 << 34) + 1), 1), (dict(lr_scale=math.nan), 1), (dict(weight_decay=math.inf), 1),
+    (dict(n=(1 << 34) + 1), 1), (dict(grad=1 << 48), 1), (dict(param=(1 << 63) + FAKE), 1), (dict(lr_scale=math.nan), 1), (dict(weight_decay=math.inf), 1),
     (dict(master=FAKE), 2), (dict(param_dtype=BF16, master=FAKE + 2), 1), (dict(param_dtype=E4M3), 2),
     (dict(grad_dtype=E4M3), 2), (dict(grad_dtype=5), 2)])
 def test_adamw_tensor(lib, over, code):

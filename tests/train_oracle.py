@@ -109,12 +109,12 @@ def stochastic_bf16(v, bits16):
 
 
 def stochastic_e4m3(t, bits16):
-    """Codes of t moved down or up: floor(|t| / step + u) step."""
-    a = np.abs(t.astype(np.float32))
+    """Codes of t moved down or up: floor(|t| / step + u) step, without
+    rounding on the way."""
+    a = np.abs(t.astype(np.float64))
     _, e = np.frexp(a)
     e = np.maximum(e - 1, -6)
-    u = bits16.astype(np.float32) / np.float32(65536)
-    k = np.floor((np.ldexp(a, 3 - e).astype(np.float32) + u).astype(np.float32))
+    k = np.floor(np.ldexp(a, 3 - e) + bits16.astype(np.float64) / 65536)
     v = np.minimum(np.ldexp(k, e - 3), 448.0)
     return e4m3_nearest(np.copysign(v, t))
 
@@ -126,7 +126,7 @@ def blocks(x):
 def quantise(x, bits16, floor):
     """(codes, scale) of a moment; bits16 None: to nearest."""
     f = np.float32
-    s = np.maximum(np.abs(blocks(x)).max(axis=1) / f(448), f(TINY)).astype(f)
+    s = np.maximum(np.abs(blocks(x)).max(axis=1) * (f(1) / f(448)), f(TINY)).astype(f)
     inv = (f(1) / s).astype(f)
     t = (blocks(x) * inv[:, None]).reshape(-1)[:len(x)].astype(f)
     codes = e4m3_nearest(t) if bits16 is None else stochastic_e4m3(t, bits16)
