@@ -9,6 +9,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -225,13 +226,16 @@ def _torch():
     return torch
 
 
-def _dtype_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.float32:
+def _type_code(dtype, torch) -> int:
+    if dtype is torch.float32:
         return DTYPE_F32
-    if t.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return DTYPE_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _dtype_code(t) -> int:
+    return _type_code(t.dtype, _torch())
 
 
 def _dims(t, n, what):
@@ -602,15 +606,22 @@ class RmsNormGrad(NamedTuple):
     dweight: object  # [d] float32
 
 
-def _here(device, stream):
+# Descriptors of sizes the library only reads: one for each set of values.
+_norm_shape = functools.lru_cache(maxsize=256)(NormShape)
+
+
+def _here(t, stream):
     """The handle of the stream to launch on: `stream`, or the current one.
     The library launches on the current device, so tensors must be there."""
     torch = _torch()
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, not {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, which is not the current device")
-    return torch.cuda.current_stream().cuda_stream if stream is None else int(stream.cuda_stream)
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a GPU, not {t.device}")
+    index = t.get_device()
+    if index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, which is not the current device")
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(shape, dtype, device, stream):
@@ -624,12 +635,10 @@ def _empty(shape, dtype, device, stream):
 
 def _tensor(t, shape, dtype, device, what):
     """The pointer of a tensor that must have this shape, dtype and device
-    and be contiguous; 0 for None."""
-    if t is None:
-        return 0
+    and be contiguous."""
     if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}, got {t.device}")
@@ -650,56 +659,70 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
     that dtype) gives y in 8 bits with a scale per row, or per ``group`` = 32,
     64 or 128 columns.  ``residual_out`` may be ``residual`` itself."""
     torch = _torch()
-    T, d = _dims(x, 2, "x [T,d]")
     shape, dev = x.shape, x.device
-    ty = weight.dtype if weight is not None else x.dtype
-    code = _dtype_code(weight if weight is not None else x)
+    if len(shape) != 2:
+        raise ValueError(f"x [T,d] must have 2 dimensions, got shape {tuple(shape)}")
+    T, d = shape
+    xty = x.dtype
+    px, pr, pw, pz, prs, ps = _tensor(x, shape, xty, dev, "x"), 0, 0, 0, 0, 0
+    ty = xty if weight is None else weight.dtype
+    if weight is not None:
+        pw = _tensor(weight, (d,), ty, dev, "weight [d]")
     if residual is None:
-        stream_ty, stream_code = x.dtype, _dtype_code(x)
+        stream_ty = xty
     else:
-        stream_ty, stream_code = residual.dtype, _dtype_code(residual)
-        if x.dtype != ty:
-            raise ValueError(f"x must be {ty} beside a residual, got {x.dtype}")
+        stream_ty = residual.dtype
+        pr = _tensor(residual, shape, stream_ty, dev, "residual")
+        if xty is not ty:
+            raise ValueError(f"x must be {ty} beside a residual, got {xty}")
+    code, stream_code = _type_code(ty, torch), _type_code(stream_ty, torch)
     out_ty = y.dtype if y is not None else (out_dtype or ty)
-    if out_dtype is not None and out_ty != out_dtype:
+    if out_dtype is not None and out_ty is not out_dtype:
         raise ValueError(f"y must be {out_dtype}, got {out_ty}")
-    e4m3 = out_ty == torch.float8_e4m3fn
-    if not e4m3 and out_ty != ty:
+    e4m3 = out_ty is torch.float8_e4m3fn
+    if not e4m3 and out_ty is not ty:
         raise ValueError(f"y must be {ty} or torch.float8_e4m3fn, got {out_ty}")
-    px = _tensor(x, shape, x.dtype, dev, "x")
-    pr = _tensor(residual, shape, stream_ty, dev, "residual")
-    pw = _tensor(weight, (d,), ty, dev, "weight [d]")
-    handle = _here(dev, stream)
-    if residual is None and stream_ty != ty:  # x is the stream itself
+    handle = _here(x, stream)
+    if residual is None and stream_ty is not ty:  # x is the stream itself
         px, pr = 0, px
     if y is None:
         y = _empty(shape, out_ty, dev, stream)
-    py = _tensor(y, shape, out_ty, dev, "y")
-    if residual is not None and residual_out is None:
+        py = y.data_ptr()
+    else:
+        py = _tensor(y, shape, out_ty, dev, "y")
+    if residual_out is not None:
+        pz = _tensor(residual_out, shape, stream_ty, dev, "residual_out")
+    elif residual is not None:
         residual_out = _empty(shape, stream_ty, dev, stream)
-    pz = _tensor(residual_out, shape, stream_ty, dev, "residual_out")
-    if rstd is None and want_rstd:
+        pz = residual_out.data_ptr()
+    if rstd is not None:
+        prs = _tensor(rstd, (T,), torch.float32, dev, "rstd [T]")
+    elif want_rstd:
         rstd = _empty((T,), torch.float32, dev, stream)
-    ps = 0
+        prs = rstd.data_ptr()
     if e4m3:
         groups = (T, -(-d // group) if group > 0 else 1)
         if scale is None:
             scale = _empty(groups, torch.float32, dev, stream)
-        ps = _tensor(scale, groups, torch.float32, dev, "scale [T, groups]")
+            ps = scale.data_ptr()
+        else:
+            ps = _tensor(scale, groups, torch.float32, dev, "scale [T, groups]")
     elif scale is not None:
         raise ValueError("scale is for a y of torch.float8_e4m3fn")
     st = load_library().fff_rms_norm(
-        NormShape(T, d, code, stream_code, DTYPE_E4M3 if e4m3 else code, group, eps, weight_offset),
-        px, pr, pw, py, ps, pz, _tensor(rstd, (T,), torch.float32, dev, "rstd [T]"), handle)
+        _norm_shape(T, d, code, stream_code, DTYPE_E4M3 if e4m3 else code, group, eps, weight_offset),
+        px, pr, pw, py, ps, pz, prs, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_rms_norm")
     return RmsNorm(y, residual_out, rstd, scale)
 
 
-def rms_norm_backward_workspace_size(T: int, d: int) -> int:
+@functools.lru_cache(maxsize=256)
+def rms_norm_backward_workspace_size(T: int, d: int, dtype: int, stream_dtype: int) -> int:
+    """Workspace bytes of rms_norm_backward (dtypes: fff_dtype_t codes)."""
     n = ctypes.c_size_t()
     st = load_library().fff_rms_norm_backward_workspace_size(
-        NormShape(T, d, DTYPE_F32, DTYPE_F32, DTYPE_F32, 0, 0.0, 0.0), ctypes.byref(n))
+        NormShape(T, d, dtype, stream_dtype, dtype, 0, 0.0, 0.0), ctypes.byref(n))
     if st != SUCCESS:
         raise FFFError(st, "fff_rms_norm_backward_workspace_size")
     return n.value
@@ -713,34 +736,44 @@ def rms_norm_backward(dy, z, weight, rstd, *, dresidual=None, weight_offset: flo
     ``dresidual`` the gradient that reaches residual_out.  Where z is float32
     beside a bf16 layer, dx is dz once more in bf16."""
     torch = _torch()
-    T, d = _dims(dy, 2, "dy [T,d]")
     shape, dev = dy.shape, dy.device
-    ty, code = dy.dtype, _dtype_code(dy)
-    zty, zcode = z.dtype, _dtype_code(z)
-    f32 = torch.float32
+    if len(shape) != 2:
+        raise ValueError(f"dy [T,d] must have 2 dimensions, got shape {tuple(shape)}")
+    T, d = shape
+    ty, zty, f32 = dy.dtype, z.dtype, torch.float32
     pdy = _tensor(dy, shape, ty, dev, "dy")
     pz = _tensor(z, shape, zty, dev, "z")
-    pw = _tensor(weight, (d,), ty, dev, "weight [d]")
+    pw = _tensor(weight, (d,), ty, dev, "weight [d]") if weight is not None else 0
     pr = _tensor(rstd, (T,), f32, dev, "rstd [T]")
-    pe = _tensor(dresidual, shape, zty, dev, "dresidual")
-    handle = _here(dev, stream)
+    pe = _tensor(dresidual, shape, zty, dev, "dresidual") if dresidual is not None else 0
+    code, zcode = _type_code(ty, torch), _type_code(zty, torch)
+    handle = _here(dy, stream)
+    pdx = pdw = pws = have = 0
     if dz is None:
         dz = _empty(shape, zty, dev, stream)
-    if dx is None and zty != ty:
+        pdz = dz.data_ptr()
+    else:
+        pdz = _tensor(dz, shape, zty, dev, "dz")
+    if dx is not None:
+        pdx = _tensor(dx, shape, ty, dev, "dx")
+    elif zty is not ty:
         dx = _empty(shape, ty, dev, stream)
-    if dweight is None and want_dweight:
+        pdx = dx.data_ptr()
+    if dweight is not None:
+        pdw = _tensor(dweight, (d,), f32, dev, "dweight [d]")
+    elif want_dweight:
         dweight = _empty((d,), f32, dev, stream)
-    need = rms_norm_backward_workspace_size(T, d) if dweight is not None else 0
-    if workspace is None and need:
-        workspace = _empty((need,), torch.uint8, dev, stream)
+        pdw = dweight.data_ptr()
     if workspace is not None:
-        _check([workspace], torch.uint8, dev)
+        have = workspace.numel()
+        pws = _tensor(workspace, (have,), torch.uint8, dev, "workspace")
+    elif dweight is not None:
+        have = rms_norm_backward_workspace_size(T, d, code, zcode)
+        workspace = _empty((have,), torch.uint8, dev, stream)
+        pws = workspace.data_ptr()
     st = load_library().fff_rms_norm_backward(
-        NormShape(T, d, code, zcode, code, 0, 0.0, weight_offset), pdy, pz, pw, pr, pe,
-        _tensor(dz, shape, zty, dev, "dz"), _tensor(dx, shape, ty, dev, "dx"),
-        _tensor(dweight, (d,), f32, dev, "dweight [d]"),
-        workspace.data_ptr() if workspace is not None else 0,
-        workspace.numel() if workspace is not None else 0, handle)
+        _norm_shape(T, d, code, zcode, code, 0, 0.0, weight_offset), pdy, pz, pw, pr, pe, pdz, pdx,
+        pdw, pws, have, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_rms_norm_backward")
     return RmsNormGrad(dz, dz if dx is None else dx, dweight)
@@ -752,10 +785,11 @@ class TensorTable:
     alive; they are updated in place and must keep their storage (make
     another table where a tensor is replaced)."""
 
-    def __init__(self, entries, device, state_code, keep):
+    def __init__(self, entries, first, state_code, keep):
         self.entries = entries        # array of AdamwTensor
         self.count = len(entries)
-        self.device = device
+        self.first = first            # the first tensor, for its device
+        self.device = first.device
         self.state_code = state_code  # None: gradients only
         self.keep = keep
         n = ctypes.c_size_t()
@@ -795,7 +829,7 @@ def grad_table(grads) -> TensorTable:
     for i, (e, g) in enumerate(zip(entries, grads)):
         e.grad = _flat(g, g.numel(), (torch.float32, torch.bfloat16), grads[0].device, f"grads[{i}]")
         e.n, e.grad_dtype = g.numel(), _dtype_code(g)
-    return TensorTable(entries, grads[0].device, None, grads)
+    return TensorTable(entries, grads[0], None, grads)
 
 
 def adamw_state(params, bits: int = 32):
@@ -855,7 +889,7 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
         if e4m3:
             e.scale = _flat(sc, 2 * -(-e.n // ADAMW_BLOCK), f32, dev, f"scales[{i}]")
         e.lr_scale, e.weight_decay = float(shares[i]), float(decays[i])
-    return TensorTable(entries, dev, DTYPE_E4M3 if e4m3 else DTYPE_F32, (params, lists))
+    return TensorTable(entries, params[0], DTYPE_E4M3 if e4m3 else DTYPE_F32, (params, lists))
 
 
 def adamw_step(table: TensorTable, *, lr: float, step: int, beta1: float = 0.9,
@@ -873,7 +907,7 @@ def adamw_step(table: TensorTable, *, lr: float, step: int, beta1: float = 0.9,
     ps = 0
     if grad_scale is not None:
         ps = _flat(grad_scale, 1, (torch.float32,), table.device, "grad_scale")
-    handle = _here(table.device, stream)
+    handle = _here(table.first, stream)
     config = AdamwConfig(lr, beta1, beta2, eps, step, table.state_code, seed is not None,
                          0 if seed is None else seed & 0xFFFFFFFFFFFFFFFF, ps)
     st = load_library().fff_adamw_step(config, table.entries, table.count, handle)
@@ -889,17 +923,21 @@ def grad_norm(grads, *, max_norm: float = float("inf"), out=None, workspace=None
     torch = _torch()
     table = grads if isinstance(grads, TensorTable) else grad_table(grads)
     dev = table.device
-    handle = _here(dev, stream)
+    handle = _here(table.first, stream)
+    pws = have = 0
     if out is None:
         out = _empty((2,), torch.float32, dev, stream)
-    if workspace is None and table.norm_workspace:
-        workspace = _empty((table.norm_workspace,), torch.uint8, dev, stream)
+        pout = out.data_ptr()
+    else:
+        pout = _tensor(out, (2,), torch.float32, dev, "out [2]")
     if workspace is not None:
-        _check([workspace], torch.uint8, dev)
-    st = load_library().fff_grad_norm(
-        table.entries, table.count, max_norm, _tensor(out, (2,), torch.float32, dev, "out [2]"),
-        workspace.data_ptr() if workspace is not None else 0,
-        workspace.numel() if workspace is not None else 0, handle)
+        have = workspace.numel()
+        pws = _tensor(workspace, (have,), torch.uint8, dev, "workspace")
+    elif table.norm_workspace:
+        have = table.norm_workspace
+        workspace = _empty((have,), torch.uint8, dev, stream)
+        pws = workspace.data_ptr()
+    st = load_library().fff_grad_norm(table.entries, table.count, max_norm, pout, pws, have, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_grad_norm")
     return out

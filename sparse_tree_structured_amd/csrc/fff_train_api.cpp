@@ -129,8 +129,9 @@ fff_status_t fff_rms_norm_backward_workspace_size(const fff_norm_shape_t* shape,
   fff_status_t st = check_norm(shape);
   if (st != FFF_SUCCESS) return st;
   if (!bytes) return FFF_ERROR_INVALID_VALUE;
-  *bytes = shape->T == 0 ? 0 : fff::rms_norm_backward_partials(shape->T, shape->d) *
-                                   size_t(shape->d) * sizeof(float);
+  *bytes = fff::rms_norm_backward_partials(shape->T, shape->d, shape->dtype == FFF_DTYPE_BF16,
+                                           shape->stream_dtype == FFF_DTYPE_BF16) *
+           size_t(shape->d) * sizeof(float);
   return FFF_SUCCESS;
 }
 

@@ -25,7 +25,15 @@ namespace fff {
 namespace {
 
 constexpr int kThreads = 256;
-static_assert(kAdamwChunk == kThreads * 8 && kStateBlock == 16 * 8, "16 lanes hold a block");
+// From this many bytes on a launch reads and writes past the caches: nothing
+// of it is used again before the next step.  A layer's 17.2 M elements with
+// masters take 86.6 us instead of 97.2 (8-bit states: 54.2 and 60.1), 195 MB
+// 34.6 instead of 35.9; 97 MB, which the 256 MB last-level cache can hold for
+// the next reader, 19.3 instead of 16.7, and 117 MB 23.4 instead of 21.5.
+constexpr int64_t kStreamBytes = int64_t(160) << 20;
+constexpr int kV = 4;  // consecutive elements of a lane: 16 bytes in 32 bits
+constexpr int kQuads = kAdamwChunk / (kThreads * kV);
+static_assert(kStateBlock == 32 * kV, "32 lanes hold a block");
 
 constexpr uint32_t kFirstMask = (1u << kFirstBits) - 1;
 
@@ -53,118 +61,146 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-// Eight elements from i0 on; n of them (8 where FULL) belong to the tensor.
-template <int PARAM, typename G, bool E4M3, bool STOCHASTIC, bool FULL>
-__device__ __forceinline__ void adamw_eight(const AdamwArgs& a, const AdamwEntry& t, int64_t size,
-                                            int64_t i0) {
+// What a lane has of one quad: its elements, as loaded and then as updated.
+template <typename P, typename G, bool E4M3>
+struct Quad {
+  using State = typename std::conditional<E4M3, uint8_t, float>::type;
+  int64_t i0;
+  int n;  // of its four elements, how many the tensor has
+  Pack<P, kV> p;
+  Pack<G, kV> g;
+  Pack<State, kV> m, v;
+  f32x2_t scale;
+};
+
+// One chunk of one tensor (FULL: all of it inside the tensor, which then
+// needs no tests for the end).  A lane's quads are kThreads * kV apart, so
+// that every access of a wavefront is contiguous; all are loaded before the
+// first is used.
+template <int PARAM, typename G, bool E4M3, bool STOCHASTIC, bool STREAM, bool FULL>
+__device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry& t, int64_t size,
+                                            int64_t begin) {
 #pragma clang fp contract(off)
-  const int n = FULL || size - i0 >= 8 ? 8 : static_cast<int>(size - i0 > 0 ? size - i0 : 0);
   using P = typename std::conditional<PARAM == kParamBf16, uint16_t, float>::type;
-  P* const p = t.get<P>(PARAM == kParamMaster ? t.kMaster : t.kParam) + i0;
-  Eight<P> pr;
-  Eight<G> gr;
-  load_eight(pr, static_cast<const P*>(p), n);
-  load_eight(gr, t.get<const G>(t.kGrad) + i0, n);
-  float m[8], r[8];
-  uint8_t* const mq = t.get<uint8_t>(t.kExpAvg) + i0;
-  uint8_t* const rq = t.get<uint8_t>(t.kExpAvgSq) + i0;
-  float* const mf = t.get<float>(t.kExpAvg) + i0;
-  float* const vf = t.get<float>(t.kExpAvgSq) + i0;
-  f32x2_t* const scale = t.get<f32x2_t>(t.kScale) + i0 / kStateBlock;
-  if constexpr (E4M3) {
-    EightE4m3 qm, qr;
-    qm.load(mq, n);
-    qr.load(rq, n);
-    f32x2_t sc = {0.0f, 0.0f};
-    if (n > 0) sc = *scale;
-    qm.get(m);
-    qr.get(r);
+  using Q = Quad<P, G, E4M3>;
+  using State = typename Q::State;
+  P* const p = t.get<P>(PARAM == kParamMaster ? t.kMaster : t.kParam);
+  const G* const grad = t.get<const G>(t.kGrad);
+  State* const ms = t.get<State>(t.kExpAvg);
+  State* const vs = t.get<State>(t.kExpAvgSq);
+  float* const scales = t.get<float>(t.kScale);
+  Q q[kQuads];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] *= sc[0];
-      r[i] *= sc[1];
-      r[i] *= r[i];
-    }
-  } else {
-    Eight<float> em, ev;
-    load_eight(em, static_cast<const float*>(mf), n);
-    load_eight(ev, static_cast<const float*>(vf), n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = em.get(i);
-      r[i] = ev.get(i);
-    }
+  for (int k = 0; k < kQuads; ++k) {
+    q[k].i0 = begin + (k * kThreads + threadIdx.x) * kV;
+    const int64_t left = size - q[k].i0;
+    const int n = q[k].n = FULL || left >= kV ? kV : static_cast<int>(left > 0 ? left : 0);
+    q[k].p.template load<STREAM>(p + q[k].i0, n);
+    q[k].g.template load<STREAM>(grad + q[k].i0, n);
+    q[k].m.template load<STREAM>(ms + q[k].i0, n);
+    q[k].v.template load<STREAM>(vs + q[k].i0, n);
+    q[k].scale = f32x2_t{0.0f, 0.0f};
+    if (E4M3 && n > 0)
+      q[k].scale = *reinterpret_cast<const f32x2_t*>(scales + q[k].i0 / kStateBlock * 2);
   }
   float gs = 1.0f;
   if (a.grad_scale) gs = *a.grad_scale;
-  float w[8];
-  uint32_t top_m = 0, top_r = 0;
+  if (gs != gs) return;  // the gradient's norm was not finite: no step
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float g = gr.get(i) * gs;
-    m[i] = m[i] * a.beta1 + g * a.one_beta1;
-    const float v = r[i] * a.beta2 + (g * g) * a.one_beta2;
-    const float root = sqrtf(v);
-    w[i] = pr.get(i) * t.decay - t.step * (m[i] / (root * a.root + a.eps));
-    r[i] = E4M3 ? root : v;
-    if (E4M3) {
+  for (int k = 0; k < kQuads; ++k) {
+    const int64_t i0 = q[k].i0;
+    const int n = q[k].n;
+    float m[kV], r[kV], w[kV];
+    if constexpr (E4M3) {
+      unpack_e4m3(q[k].m, m);
+      unpack_e4m3(q[k].v, r);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        m[i] *= q[k].scale[0];
+        r[i] *= q[k].scale[1];
+        r[i] *= r[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        m[i] = q[k].m.get(i);
+        r[i] = q[k].v.get(i);
+      }
+    }
+    uint32_t top_m = 0, top_r = 0;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const float g = q[k].g.get(i) * gs;
+      m[i] = m[i] * a.beta1 + g * a.one_beta1;
+      const float v = r[i] * a.beta2 + (g * g) * a.one_beta2;
+      const float root = sqrtf(v);
+      w[i] = q[k].p.get(i) * t.decay - t.step * (m[i] / (root * a.root + a.eps));
+      r[i] = E4M3 ? root : v;
       top_m = umax(top_m, size_bits(m[i]));
       top_r = umax(top_r, __float_as_uint(root));  // root >= 0, or NaN
     }
-  }
-  if (gs != gs) return;  // the gradient's norm was not finite: no step
-  uint32_t h[8], rnd[8];
-  if constexpr (STOCHASTIC) {
-    const uint32_t base = t.key ^ (static_cast<uint32_t>(i0 >> 32) * 0x9E3779B9u);
+    uint32_t h[kV], rnd[kV];
+    if constexpr (STOCHASTIC) {
+      const uint32_t base = t.key ^ (static_cast<uint32_t>(i0 >> 32) * 0x9E3779B9u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = mix32((static_cast<uint32_t>(i0) + i) ^ base);
-  }
-  if constexpr (PARAM == kParamMaster) store_eight(t.get<uint16_t>(t.kParam) + i0, n, w);
-  if constexpr (PARAM == kParamBf16 && STOCHASTIC) {
+      for (int i = 0; i < kV; ++i) h[i] = mix32((static_cast<uint32_t>(i0) + i) ^ base);
+    }
+    if constexpr (PARAM == kParamMaster)
+      packed<uint16_t, kV>(w).template store<STREAM>(t.get<uint16_t>(t.kParam) + i0, n);
+    if constexpr (PARAM == kParamBf16 && STOCHASTIC) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rnd[i] = mix32(h[i] ^ 0x9E3779B9u) << 16;
-    store_packed(p, n, pack_bf16_stochastic(w, rnd));
-  } else {
-    store_eight(p, n, w);
-  }
-  if constexpr (!E4M3) {
-    store_eight(mf, n, m);
-    store_eight(vf, n, r);
-    return;
-  }
-  // Lanes past the tensor's end hold zeros, which no maximum sees.
-  const float sm = e4m3_scale(group_max<16>(top_m));
-  const float sr = e4m3_scale(group_max<16>(top_r));
-  const float im = 1.0f / sm, ir = 1.0f / sr;
+      for (int i = 0; i < kV; ++i) rnd[i] = mix32(h[i] ^ 0x9E3779B9u) << 16;
+      pack_bf16_stochastic(w, rnd).template store<STREAM>(p + i0, n);
+    } else {
+      packed<P, kV>(w).template store<STREAM>(p + i0, n);
+    }
+    if constexpr (!E4M3) {
+      packed<float, kV>(m).template store<STREAM>(ms + i0, n);
+      packed<float, kV>(r).template store<STREAM>(vs + i0, n);
+      continue;
+    }
+    // The block's 32 lanes are two rows of 16.  One swap of the rows leaves
+    // both maxima of m in the first row and both of r in the second, so that
+    // one division serves both scales; another gives every lane both.
+    // Lanes past the tensor's end hold zeros, which no maximum sees.
+    const auto top = __builtin_amdgcn_permlane16_swap(group_max<16>(top_m), group_max<16>(top_r),
+                                                      false, false);
+    const float scale = e4m3_scale(umax(top[0], top[1]));
+    const float inv = 1.0f / scale;
+    const auto both = __builtin_amdgcn_permlane16_swap(__float_as_uint(inv), __float_as_uint(inv),
+                                                       false, false);
+    const float im = __uint_as_float(both[0]), ir = __uint_as_float(both[1]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m[i] *= im;
-    r[i] *= ir;
-    // at least the smallest code, which every rounding of it keeps
-    r[i] = r[i] > 0.0f ? fmaxf(r[i], 0.001953125f) : r[i];
-  }
-  u32x2_t qm, qr;
-  if constexpr (STOCHASTIC) {
+    for (int i = 0; i < kV; ++i) {
+      m[i] *= im;
+      r[i] *= ir;
+      // at least the smallest code, which every rounding of it keeps
+      r[i] = r[i] > 0.0f ? fmaxf(r[i], 0.001953125f) : r[i];
+    }
+    Pack<uint8_t, kV> qm, qr;
+    if constexpr (STOCHASTIC) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rnd[i] = h[i] << 16;
-    qm = pack_e4m3_stochastic(m, rnd);
+      for (int i = 0; i < kV; ++i) rnd[i] = h[i] << 16;
+      qm = pack_e4m3_stochastic(m, rnd);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rnd[i] = h[i] & 0xffff0000u;
-    qr = pack_e4m3_stochastic(r, rnd);
-  } else {
-    qm = pack_e4m3(m);
-    qr = pack_e4m3(r);
-  }
-  if (n > 0) {
-    store_packed(mq, n, qm);
-    store_packed(rq, n, qr);
-    if (threadIdx.x % 16 == 0) *scale = f32x2_t{sm, sr};
+      for (int i = 0; i < kV; ++i) rnd[i] = h[i] & 0xffff0000u;
+      qr = pack_e4m3_stochastic(r, rnd);
+    } else {
+      qm = pack_e4m3(m);
+      qr = pack_e4m3(r);
+    }
+    if constexpr (E4M3) {
+      qm.template store<STREAM>(ms + i0, n);
+      qr.template store<STREAM>(vs + i0, n);
+      // the first lane of either row; the block's first element is in the first one
+      const int64_t block = i0 / kStateBlock;
+      if (threadIdx.x % 16 == 0 && block * kStateBlock < size)
+        scales[2 * block + (threadIdx.x / 16) % 2] = scale;
+    }
   }
 }
 
-// One chunk of one tensor.  A chunk inside its tensor runs without any tests
-// for the tensor's end.
-template <int PARAM, typename G, bool E4M3, bool STOCHASTIC>
+template <int PARAM, typename G, bool E4M3, bool STOCHASTIC, bool STREAM>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   const int at = entry_of(a.first, a.count, blockIdx.x);
   const AdamwEntry& t = a.e[at];
@@ -172,9 +208,24 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   const int64_t size = int64_t(first >> kFirstBits) << 32 | t.n_lo;
   const int64_t begin = int64_t(blockIdx.x - (first & kFirstMask)) * kAdamwChunk;
   if (size - begin >= kAdamwChunk)
-    adamw_eight<PARAM, G, E4M3, STOCHASTIC, true>(a, t, size, begin + threadIdx.x * 8);
+    adamw_chunk<PARAM, G, E4M3, STOCHASTIC, STREAM, true>(a, t, size, begin);
   else
-    adamw_eight<PARAM, G, E4M3, STOCHASTIC, false>(a, t, size, begin + threadIdx.x * 8);
+    adamw_chunk<PARAM, G, E4M3, STOCHASTIC, STREAM, false>(a, t, size, begin);
+}
+
+// A lane's share of the squares of a chunk of one tensor, 16 bytes at a time.
+template <typename E, int V>
+__device__ __forceinline__ double squares(const E* grad, int64_t n, int64_t begin) {
+  double s = 0.0;
+#pragma unroll 4
+  for (int k = 0; k < kNormChunk / (kThreads * V); ++k) {
+    const int64_t i0 = begin + (k * kThreads + threadIdx.x) * V;
+    Pack<E, V> g;
+    g.load(grad + i0, n - i0 >= V ? V : static_cast<int>(n - i0 > 0 ? n - i0 : 0));
+#pragma unroll
+    for (int i = 0; i < V; ++i) s += static_cast<double>(g.get(i)) * g.get(i);
+  }
+  return s;
 }
 
 // Sum of squares of one chunk of one tensor, in 64 bits: neither a large
@@ -186,22 +237,10 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) 
   const int64_t n = bf16 ? -t.n : t.n;
   const int64_t begin = int64_t(blockIdx.x - a.first[at]) * kNormChunk;
   double s = 0.0;
-#pragma unroll 4
-  for (int k = 0; k < kNormChunk / (kThreads * 8); ++k) {
-    const int64_t i0 = begin + (k * kThreads + threadIdx.x) * 8;
-    const int m = n - i0 >= 8 ? 8 : static_cast<int>(n - i0 > 0 ? n - i0 : 0);
-    if (bf16) {
-      Eight<uint16_t> g;
-      load_eight(g, static_cast<const uint16_t*>(t.grad) + i0, m);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += static_cast<double>(g.get(i)) * g.get(i);
-    } else {
-      Eight<float> g;
-      load_eight(g, static_cast<const float*>(t.grad) + i0, m);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += static_cast<double>(g.get(i)) * g.get(i);
-    }
-  }
+  if (bf16)
+    s = squares<uint16_t, 8>(static_cast<const uint16_t*>(t.grad), n, begin);
+  else
+    s = squares<float, 4>(static_cast<const float*>(t.grad), n, begin);
   __shared__ double lds[kThreads / kWave];
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, kWave);
@@ -230,37 +269,48 @@ __global__ __launch_bounds__(1024) void grad_norm_final_kernel(const double* par
   }
 }
 
-template <int PARAM, typename G>
+template <int PARAM, typename G, bool STREAM>
 void launch_states(const AdamwArgs& a, int blocks, bool e4m3, bool stochastic, hipStream_t st) {
   if (e4m3 && stochastic)
-    adamw_kernel<PARAM, G, true, true><<<blocks, kThreads, 0, st>>>(a);
+    adamw_kernel<PARAM, G, true, true, STREAM><<<blocks, kThreads, 0, st>>>(a);
   else if (e4m3)
-    adamw_kernel<PARAM, G, true, false><<<blocks, kThreads, 0, st>>>(a);
+    adamw_kernel<PARAM, G, true, false, STREAM><<<blocks, kThreads, 0, st>>>(a);
   else if (stochastic && PARAM == kParamBf16)
-    adamw_kernel<PARAM, G, false, PARAM == kParamBf16><<<blocks, kThreads, 0, st>>>(a);
+    adamw_kernel<PARAM, G, false, PARAM == kParamBf16, STREAM><<<blocks, kThreads, 0, st>>>(a);
   else  // nothing in this case is rounded stochastically
-    adamw_kernel<PARAM, G, false, false><<<blocks, kThreads, 0, st>>>(a);
+    adamw_kernel<PARAM, G, false, false, STREAM><<<blocks, kThreads, 0, st>>>(a);
 }
 
-template <int PARAM>
+template <int PARAM, bool STREAM>
 void launch_grads(const AdamwArgs& a, int blocks, bool grad_bf16, bool e4m3, bool stochastic,
                   hipStream_t st) {
   if (grad_bf16)
-    launch_states<PARAM, uint16_t>(a, blocks, e4m3, stochastic, st);
+    launch_states<PARAM, uint16_t, STREAM>(a, blocks, e4m3, stochastic, st);
   else
-    launch_states<PARAM, float>(a, blocks, e4m3, stochastic, st);
+    launch_states<PARAM, float, STREAM>(a, blocks, e4m3, stochastic, st);
+}
+
+template <bool STREAM>
+void launch_params(const AdamwArgs& a, int blocks, int param, bool grad_bf16, bool e4m3,
+                   bool stochastic, hipStream_t st) {
+  if (param == kParamF32)
+    launch_grads<kParamF32, STREAM>(a, blocks, grad_bf16, e4m3, stochastic, st);
+  else if (param == kParamBf16)
+    launch_grads<kParamBf16, STREAM>(a, blocks, grad_bf16, e4m3, stochastic, st);
+  else
+    launch_grads<kParamMaster, STREAM>(a, blocks, grad_bf16, e4m3, stochastic, st);
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const AdamwArgs& a, int blocks, int param, bool grad_bf16, bool state_e4m3,
                         bool stochastic, hipStream_t st) {
-  if (param == kParamF32)
-    launch_grads<kParamF32>(a, blocks, grad_bf16, state_e4m3, stochastic, st);
-  else if (param == kParamBf16)
-    launch_grads<kParamBf16>(a, blocks, grad_bf16, state_e4m3, stochastic, st);
+  const int64_t each = (param == kParamF32 ? 8 : param == kParamBf16 ? 4 : 10) +
+                       (grad_bf16 ? 2 : 4) + (state_e4m3 ? 4 : 16);
+  if (blocks * kAdamwChunk * each >= kStreamBytes)
+    launch_params<true>(a, blocks, param, grad_bf16, state_e4m3, stochastic, st);
   else
-    launch_grads<kParamMaster>(a, blocks, grad_bf16, state_e4m3, stochastic, st);
+    launch_params<false>(a, blocks, param, grad_bf16, state_e4m3, stochastic, st);
   return hipGetLastError();
 }
 

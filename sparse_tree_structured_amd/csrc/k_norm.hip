@@ -5,10 +5,11 @@
 //   g = dy (w + offset);  dz = rstd (g - z rstd mean(g z rstd)) + dres
 //   dw = sum over rows of dy z rstd
 //
-// A row is held in registers by a team of one to sixteen wavefronts, eight
-// consecutive columns per lane and chunk, so it is read once: the sum of
-// squares, the output and (for e4m3) the largest size all come from the
-// registers.
+// A row is held in registers by a team of one to sixteen wavefronts, so it is
+// read once: the sum of squares, the output and (for e4m3) the largest size
+// all come from the registers.  A lane has four consecutive columns in each
+// chunk of a row, or eight where every type is 16 bits wide (16-byte accesses
+// either way, contiguous over the wavefront).
 #include "common.hpp"
 #include "launch_train.hpp"
 #include "train.hpp"
@@ -49,8 +50,21 @@ __device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* lds) {
 
 constexpr int block_threads(int waves) { return waves == 1 ? 4 * kWave : waves * kWave; }
 
+// Columns of a lane in one chunk.
+template <typename X, typename S>
+constexpr int kCols = sizeof(X) == 2 && sizeof(S) == 2 ? 8 : 4;
+
+// Lanes of one scale's group.
+template <int V>
+__device__ __forceinline__ uint32_t group_top(uint32_t v, int group) {
+  if (group == 32) return group_max<32 / V>(v);
+  if (group == 64) return group_max<64 / V>(v);
+  return group_max<128 / V>(v);
+}
+
 template <typename X, typename S, bool F8, int WAVES, int C>
 __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs a) {
+  constexpr int V = kCols<X, S>;
   constexpr int kTeam = WAVES * kWave;
   constexpr int kRows = block_threads(WAVES) / kTeam;  // rows a workgroup has at a time
   __shared__ float lds_f[WAVES];
@@ -64,31 +78,31 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
   for (int64_t t = int64_t(blockIdx.x) * kRows + threadIdx.x / kTeam; t < a.T;
        t += int64_t(gridDim.x) * kRows) {
     const size_t row = static_cast<size_t>(t) * a.d;
-    Eight<X> xr[C], wr[C];
-    Eight<S> rr[C];
+    Pack<X, V> xr[C], wr[C];
+    Pack<S, V> rr[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * kTeam + lane) * 8;
-      if (x) load_eight(xr[c], x + row + col, a.d - col);
-      if (r) load_eight(rr[c], r + row + col, a.d - col);
+      const int col = (c * kTeam + lane) * V;
+      if (x) xr[c].load(x + row + col, a.d - col);
+      if (r) rr[c].load(r + row + col, a.d - col);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * kTeam + lane) * 8;
-      if (w) load_eight(wr[c], w + col, a.d - col);
+      const int col = (c * kTeam + lane) * V;
+      if (w) wr[c].load(w + col, a.d - col);
     }
-    float z[C][8];
+    float z[C][V];
     float ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * kTeam + lane) * 8;
+      const int col = (c * kTeam + lane) * V;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < V; ++i) {
         z[c][i] = (x ? xr[c].get(i) : 0.0f) + (r ? rr[c].get(i) : 0.0f);
         ss += z[c][i] * z[c][i];
       }
       // y is formed from the 32-bit sum; only the stored copy is rounded.
-      if (zout) store_eight(zout + row + col, a.d - col, z[c]);
+      if (zout) packed<S, V>(z[c]).store(zout + row + col, a.d - col);
     }
     ss = team_total<WAVES>(ss, lds_f);
     const float rstd = 1.0f / sqrtf(ss * inv_d + a.eps);
@@ -96,24 +110,24 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < V; ++i)
         z[c][i] = z[c][i] * rstd * ((w ? wr[c].get(i) : 1.0f) + a.weight_offset);
     if constexpr (!F8) {
       X* y = static_cast<X*>(a.y);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int col = (c * kTeam + lane) * 8;
-        store_eight(y + row + col, a.d - col, z[c]);
+        const int col = (c * kTeam + lane) * V;
+        packed<X, V>(z[c]).store(y + row + col, a.d - col);
       }
     } else {
       uint8_t* y = static_cast<uint8_t*>(a.y);
       uint32_t top[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int col = (c * kTeam + lane) * 8;
+        const int col = (c * kTeam + lane) * V;
         top[c] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < V; ++i)
           if (col + i < a.d) top[c] = umax(top[c], size_bits(z[c][i]));
       }
       if (a.group == 0) {
@@ -125,16 +139,14 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int col = (c * kTeam + lane) * 8;
-        if (a.group == 32) top[c] = group_max<4>(top[c]);
-        if (a.group == 64) top[c] = group_max<8>(top[c]);
-        if (a.group == 128) top[c] = group_max<16>(top[c]);
+        const int col = (c * kTeam + lane) * V;
+        if (a.group != 0) top[c] = group_top<V>(top[c], a.group);
         const float scale = e4m3_scale(top[c]);
         const float inv = 1.0f / scale;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[c][i] *= inv;
+        for (int i = 0; i < V; ++i) z[c][i] *= inv;
         if (col < a.d) {
-          store_packed(y + row + col, a.d - col, pack_e4m3(z[c]));
+          pack_e4m3(z[c]).store(y + row + col, a.d - col);
           if (a.group == 0) {
             if (col == 0) a.scale[t] = scale;
           } else if (col % a.group == 0) {
@@ -146,13 +158,17 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
   }
 }
 
-// One row at a time per team; the columns' share of dw stays in registers
-// over the team's rows and goes to the workspace once per workgroup.
-template <typename X, typename S, int WAVES, int C>
+// R rows at a time per team, whose dots share a barrier; the columns' share
+// of dw stays in registers over the team's rows and goes to the workspace
+// once per team.
+template <typename X, typename S, int WAVES, int C, int R, bool STREAM>
 __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_backward_kernel(NormGradArgs a) {
+  constexpr int V = kCols<X, S>;
   constexpr int kTeam = WAVES * kWave;
   constexpr int kRows = block_threads(WAVES) / kTeam;
-  __shared__ float lds_f[WAVES];
+  // Two sets, used in turn: a wavefront that is a round ahead writes the
+  // other one, and the round's barrier keeps it from being two ahead.
+  __shared__ float lds[2][R][WAVES];
   const int lane = threadIdx.x % kTeam;
   const X* dy = static_cast<const X*>(a.dy);
   const S* zin = static_cast<const S*>(a.z);
@@ -161,62 +177,97 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_backward_kernel
   S* dz = static_cast<S*>(a.dz);
   X* dx = static_cast<X*>(a.dx);
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  float gain[C][8], acc[C][8];
+  float gain[C][V], acc[C][V];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = (c * kTeam + lane) * 8;
-    Eight<X> wr;
-    if (w) load_eight(wr, w + col, a.d - col);
+    const int col = (c * kTeam + lane) * V;
+    Pack<X, V> wr;
+    if (w) wr.load(w + col, a.d - col);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < V; ++i) {
       gain[c][i] = (w ? wr.get(i) : 1.0f) + a.weight_offset;
       acc[c][i] = 0.0f;
     }
   }
-  for (int64_t t = int64_t(blockIdx.x) * kRows + threadIdx.x / kTeam; t < a.T;
-       t += int64_t(gridDim.x) * kRows) {
-    const size_t row = static_cast<size_t>(t) * a.d;
-    const float rstd = a.rstd[t];
-    Eight<X> yr[C];
-    Eight<S> zr[C], er[C];
+  const int64_t stride = int64_t(gridDim.x) * kRows;
+  int set = 0;
+  for (int64_t t0 = int64_t(blockIdx.x) * kRows + threadIdx.x / kTeam; t0 < a.T;
+       t0 += R * stride, set ^= 1) {
+    Pack<X, V> yr[R][C];
+    Pack<S, V> zr[R][C], er[R][C];
+    float rstd[R], dot[R];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * kTeam + lane) * 8;
-      load_eight(yr[c], dy + row + col, a.d - col);
-      load_eight(zr[c], zin + row + col, a.d - col);
-      if (dres) load_eight(er[c], dres + row + col, a.d - col);
+    for (int k = 0; k < R; ++k) {
+      const int64_t t = t0 + k * stride;
+      const int width = t < a.T ? a.d : 0;  // a row past the last one reads nothing
+      const size_t row = static_cast<size_t>(t) * a.d;
+      rstd[k] = t < a.T ? a.rstd[t] : 0.0f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int col = (c * kTeam + lane) * V;
+        yr[k][c].template load<STREAM>(dy + row + col, width - col);
+        zr[k][c].template load<STREAM>(zin + row + col, width - col);
+        if (dres) er[k][c].template load<STREAM>(dres + row + col, width - col);
+      }
     }
-    float dot = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int k = 0; k < R; ++k) {
+      dot[k] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float zh = zr[c].get(i) * rstd;
-        const float d = yr[c].get(i);
-        acc[c][i] += d * zh;
-        dot += d * gain[c][i] * zh;
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float zh = zr[k][c].get(i) * rstd[k];
+          const float d = yr[k][c].get(i);
+          acc[c][i] += d * zh;
+          dot[k] += d * gain[c][i] * zh;
+        }
+      dot[k] = wave_total(dot[k]);
+    }
+    if constexpr (WAVES > 1) {
+      if ((threadIdx.x & (kWave - 1)) == 0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) lds[set][k][threadIdx.x / kWave] = dot[k];
       }
-    dot = team_total<WAVES>(dot, lds_f) * inv_d;
+      __syncthreads();
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * kTeam + lane) * 8;
-      float v[8];
+      for (int k = 0; k < R; ++k) {
+        dot[k] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float zh = zr[c].get(i) * rstd;
-        v[i] = rstd * (yr[c].get(i) * gain[c][i] - zh * dot) + (dres ? er[c].get(i) : 0.0f);
+        for (int i = 0; i < WAVES; ++i) dot[k] += lds[set][k][i];
       }
-      store_eight(dz + row + col, a.d - col, v);
-      if (dx) store_eight(dx + row + col, a.d - col, v);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t t = t0 + k * stride;
+      const int width = t < a.T ? a.d : 0;
+      const size_t row = static_cast<size_t>(t) * a.d;
+      const float mean = dot[k] * inv_d;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int col = (c * kTeam + lane) * V;
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float zh = zr[k][c].get(i) * rstd[k];
+          v[i] = rstd[k] * (yr[k][c].get(i) * gain[c][i] - zh * mean) +
+                 (dres ? er[k][c].get(i) : 0.0f);
+        }
+        packed<S, V>(v).store(dz + row + col, width - col);
+        if (dx) packed<X, V>(v).store(dx + row + col, width - col);
+      }
     }
   }
   if (!a.partial) return;
-  // A workgroup of several teams stores a partial sum for each.
   float* out = a.partial + (size_t(blockIdx.x) * kRows + threadIdx.x / kTeam) * a.d;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = (c * kTeam + lane) * 8;
-    store_eight(out + col, a.d - col, acc[c]);
+    const int col = (c * kTeam + lane) * V;
+#pragma unroll
+    for (int h = 0; h < V; h += 4) {
+      const float v[4] = {acc[c][h], acc[c][h + 1], acc[c][h + 2], acc[c][h + 3]};
+      packed<float, 4>(v).store(out + col + h, a.d - col - h);
+    }
   }
 }
 
@@ -253,51 +304,105 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void rms_norm_dweight_kernel
   }
 }
 
-template <typename X, typename S, bool F8, int WAVES, int C>
-hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
-  constexpr int kRows = block_threads(WAVES) / (WAVES * kWave);
-  const int64_t blocks = (a.T + kRows - 1) / kRows;
-  const int grid = static_cast<int>(blocks < (1 << 20) ? blocks : (1 << 20));
-  rms_norm_kernel<X, S, F8, WAVES, C><<<grid, block_threads(WAVES), 0, st>>>(a);
-  return hipGetLastError();
+// Wavefronts of a row and chunks of each.
+struct RowPlan {
+  int waves, chunks;
+  int rows() const { return waves == 1 ? 4 : 1; }  // of a workgroup
+  int threads() const { return block_threads(waves); }
+};
+
+// Accesses of one wavefront that a row takes.
+int pieces_of(int d, int cols) { return (d + cols * kWave - 1) / (cols * kWave); }
+
+template <int W, int C> struct Plan {
+  static constexpr int kWaves = W, kChunks = C;
+};
+
+// Forward: two chunks per lane as long as a row fits eight wavefronts.  At
+// T = 16384, d = 2048 in bf16 2 x 2 takes 46.9 us, 4 x 1 49.1 and 1 x 4 48.2;
+// at 4096 x 8192 8 x 2 takes 47.2 and 4 x 4 49.0.
+template <typename F>
+void with_forward_plan(int pieces, const F& f) {
+  if (pieces <= 1) f(Plan<1, 1>());
+  else if (pieces <= 2) f(Plan<1, 2>());
+  else if (pieces <= 4) f(Plan<2, 2>());
+  else if (pieces <= 8) f(Plan<4, 2>());
+  else if (pieces <= 16) f(Plan<8, 2>());
+  else if (pieces <= 32) f(Plan<8, 4>());
+  else if (pieces <= 64) f(Plan<16, 4>());
+  else f(Plan<16, 8>());
 }
 
 template <typename X, typename S, bool F8>
-hipError_t pick_fwd(const NormArgs& a, hipStream_t st) {
-  if (a.d <= 512) return launch_fwd<X, S, F8, 1, 1>(a, st);
-  if (a.d <= 2048) return launch_fwd<X, S, F8, 4, 1>(a, st);
-  if (a.d <= 4096) return launch_fwd<X, S, F8, 4, 2>(a, st);
-  if (a.d <= 8192) return launch_fwd<X, S, F8, 4, 4>(a, st);
-  return launch_fwd<X, S, F8, 16, 4>(a, st);
+hipError_t run_fwd(const NormArgs& a, hipStream_t st) {
+  with_forward_plan(pieces_of(a.d, kCols<X, S>), [&](auto plan) {
+    using P = decltype(plan);
+    const RowPlan p = {P::kWaves, P::kChunks};
+    const int64_t blocks = (a.T + p.rows() - 1) / p.rows();
+    const int grid = static_cast<int>(blocks < (1 << 20) ? blocks : (1 << 20));
+    rms_norm_kernel<X, S, F8, P::kWaves, P::kChunks><<<grid, p.threads(), 0, st>>>(a);
+  });
+  return hipGetLastError();
 }
 
-struct GradPlan {
-  int waves, chunks, rows, grid;  // rows: teams per workgroup
-};
+// Backward: one chunk per lane up to four wavefronts, whose dots then share
+// a barrier for two rows.
+template <typename F>
+void with_backward_plan(int pieces, const F& f) {
+  if (pieces <= 1) f(Plan<1, 1>());
+  else if (pieces <= 2) f(Plan<2, 1>());
+  else if (pieces <= 4) f(Plan<4, 1>());
+  else if (pieces <= 8) f(Plan<4, 2>());
+  else if (pieces <= 16) f(Plan<4, 4>());
+  else if (pieces <= 32) f(Plan<8, 4>());
+  else if (pieces <= 64) f(Plan<16, 4>());
+  else f(Plan<16, 8>());
+}
 
-GradPlan grad_plan(int64_t T, int d) {
-  GradPlan p;
-  p.waves = d <= 512 ? 1 : d <= 8192 ? 4 : 16;
-  p.chunks = d <= 2048 ? 1 : d <= 4096 ? 2 : 4;
-  p.rows = p.waves == 1 ? 4 : 1;
-  const int64_t blocks = (T + p.rows - 1) / p.rows;
-  p.grid = static_cast<int>(blocks < 1024 ? blocks : 1024);
-  return p;
+// Rows of the backward at a time: two where a lane has one chunk of each.
+constexpr int grad_rows(int chunks) { return chunks == 1 ? 2 : 1; }
+
+// Workgroups of the backward: as many as keep about 48 KB of loads in flight
+// on each of the 256 compute units (every one more is another partial sum of
+// d columns to write and read), but two per compute unit, or one of more than
+// four wavefronts.  At T = 16384, d = 2048 (bf16) 512 workgroups take 48.6 us
+// with the sum of the partials, 256 take 61.4 and 1024 54.1; at 8000 x 5000
+// 512 take 71.5, 256 90.2 and 1024 76.3; at 3000 x 12288 256 take 65.5, 512
+// 72.2.
+int grad_grid(int64_t T, const RowPlan& p) {
+  constexpr int kComputeUnits = 256;
+  const int64_t blocks = (T + p.rows() - 1) / p.rows();
+  const int least = p.waves > 4 ? kComputeUnits : 2 * kComputeUnits;
+  int most = 16 * kComputeUnits / (p.threads() / kWave * p.chunks * grad_rows(p.chunks));
+  if (most < least) most = least;
+  return static_cast<int>(blocks < most ? blocks : most);
+}
+
+// From this many bytes of inputs on they are read past the caches: they would
+// push out one another and the dz that the next operator reads.  At
+// T = 16384, d = 2048 in bf16 (201 MB) that takes 54.3 us instead of 56.5,
+// and with a reader of dz behind it 71.0 instead of 77.5; at T = 4096, where
+// the inputs fit the 256 MB last-level cache, it takes 22.2 instead of 19.5.
+constexpr int64_t kGradStreamBytes = int64_t(160) << 20;
+
+int cols_of(bool bf16, bool stream_bf16) {
+  return bf16 && stream_bf16 ? kCols<uint16_t, uint16_t> : kCols<float, float>;
 }
 
 template <typename X, typename S>
-hipError_t run_bwd(const NormGradArgs& a, const GradPlan& p, hipStream_t st) {
-  const int threads = block_threads(p.waves);
-  if (p.waves == 1)
-    rms_norm_backward_kernel<X, S, 1, 1><<<p.grid, threads, 0, st>>>(a);
-  else if (p.waves == 4 && p.chunks == 1)
-    rms_norm_backward_kernel<X, S, 4, 1><<<p.grid, threads, 0, st>>>(a);
-  else if (p.waves == 4 && p.chunks == 2)
-    rms_norm_backward_kernel<X, S, 4, 2><<<p.grid, threads, 0, st>>>(a);
-  else if (p.waves == 4)
-    rms_norm_backward_kernel<X, S, 4, 4><<<p.grid, threads, 0, st>>>(a);
-  else
-    rms_norm_backward_kernel<X, S, 16, 4><<<p.grid, threads, 0, st>>>(a);
+hipError_t run_bwd(const NormGradArgs& a, hipStream_t st) {
+  with_backward_plan(pieces_of(a.d, kCols<X, S>), [&](auto plan) {
+    using P = decltype(plan);
+    constexpr int R = grad_rows(P::kChunks);
+    const RowPlan p = {P::kWaves, P::kChunks};
+    const int64_t bytes = a.T * a.d * (sizeof(X) + sizeof(S) * (a.dresidual ? 2 : 1));
+    if (bytes >= kGradStreamBytes)
+      rms_norm_backward_kernel<X, S, P::kWaves, P::kChunks, R, true>
+          <<<grad_grid(a.T, p), p.threads(), 0, st>>>(a);
+    else
+      rms_norm_backward_kernel<X, S, P::kWaves, P::kChunks, R, false>
+          <<<grad_grid(a.T, p), p.threads(), 0, st>>>(a);
+  });
   return hipGetLastError();
 }
 
@@ -305,33 +410,33 @@ hipError_t run_bwd(const NormGradArgs& a, const GradPlan& p, hipStream_t st) {
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t st) {
   if (a.bf16 && a.stream_bf16)
-    return a.e4m3 ? pick_fwd<uint16_t, uint16_t, true>(a, st)
-                  : pick_fwd<uint16_t, uint16_t, false>(a, st);
+    return a.e4m3 ? run_fwd<uint16_t, uint16_t, true>(a, st)
+                  : run_fwd<uint16_t, uint16_t, false>(a, st);
   if (a.bf16)
-    return a.e4m3 ? pick_fwd<uint16_t, float, true>(a, st)
-                  : pick_fwd<uint16_t, float, false>(a, st);
-  return a.e4m3 ? pick_fwd<float, float, true>(a, st) : pick_fwd<float, float, false>(a, st);
+    return a.e4m3 ? run_fwd<uint16_t, float, true>(a, st) : run_fwd<uint16_t, float, false>(a, st);
+  return a.e4m3 ? run_fwd<float, float, true>(a, st) : run_fwd<float, float, false>(a, st);
 }
 
-size_t rms_norm_backward_partials(int64_t T, int d) {
-  const GradPlan p = grad_plan(T, d);
-  return size_t(p.grid) * p.rows;
+size_t rms_norm_backward_partials(int64_t T, int d, bool bf16, bool stream_bf16) {
+  size_t rows = 0;
+  with_backward_plan(pieces_of(d, cols_of(bf16, stream_bf16)), [&](auto plan) {
+    const RowPlan p = {decltype(plan)::kWaves, decltype(plan)::kChunks};
+    rows = T == 0 ? 0 : size_t(grad_grid(T, p)) * p.rows();
+  });
+  return rows;
 }
 
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st) {
-  const GradPlan p = grad_plan(a.T, a.d);
-  hipError_t e = hipSuccess;
-  if (a.T == 0)
-    ;
-  else if (a.bf16 && a.stream_bf16)
-    e = run_bwd<uint16_t, uint16_t>(a, p, st);
-  else if (a.bf16)
-    e = run_bwd<uint16_t, float>(a, p, st);
-  else
-    e = run_bwd<float, float>(a, p, st);
-  if (e != hipSuccess || !a.dweight) return e;
+  if (a.T > 0) {
+    const hipError_t e = a.bf16 && a.stream_bf16 ? run_bwd<uint16_t, uint16_t>(a, st)
+                         : a.bf16                ? run_bwd<uint16_t, float>(a, st)
+                                                 : run_bwd<float, float>(a, st);
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dweight) return hipSuccess;
+  const int count = static_cast<int>(rms_norm_backward_partials(a.T, a.d, a.bf16, a.stream_bf16));
   rms_norm_dweight_kernel<<<(a.d + kSumCols - 1) / kSumCols, kSumCols * kSumSlices, 0, st>>>(
-      a.partial, a.T == 0 ? 0 : p.grid * p.rows, a.d, a.dweight);
+      a.partial, count, a.d, a.dweight);
   return hipGetLastError();
 }
 

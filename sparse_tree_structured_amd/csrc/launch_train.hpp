@@ -10,7 +10,7 @@
 
 namespace fff {
 
-constexpr int kNormMaxWidth = 32768;  // sixteen wavefronts of four chunks of 8 columns per lane
+constexpr int kNormMaxWidth = 32768;  // a row is held in one workgroup's registers
 
 struct NormArgs {
   int64_t T;
@@ -39,7 +39,8 @@ struct NormGradArgs {
   void *dz, *dx;
   float *dweight, *partial;
 };
-size_t rms_norm_backward_partials(int64_t T, int d);  // rows of d floats in the workspace
+// Rows of d floats in the workspace.
+size_t rms_norm_backward_partials(int64_t T, int d, bool bf16, bool stream_bf16);
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st);
 
 // ---- optimiser ----

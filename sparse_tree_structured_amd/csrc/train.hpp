@@ -1,88 +1,104 @@
 // Device helpers shared by the kernels around the layer (norm, optimiser):
-// eight consecutive elements per lane, reductions over lanes, e4m3.
+// consecutive elements per lane, reductions over lanes, e4m3.
 #pragma once
 
 #include "common.hpp"
 
 namespace fff {
 
-// Eight elements move as 16-byte pieces.  The declared alignment is one
-// element's: gfx950 takes unaligned global vector accesses, so rows of any
-// width and tensors that start anywhere in a buffer use the same loads.
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-typedef u32x4_t u32x4_a4_t __attribute__((aligned(4)));
-typedef u32x4_t u32x4_a2_t __attribute__((aligned(2)));
-typedef u32x2_t u32x2_a1_t __attribute__((aligned(1)));
+// A lane moves V consecutive elements (V * sizeof(E) = 4, 8 or 16 bytes) as
+// one access, so that a wavefront's access is one contiguous piece.  The
+// declared alignment is one element's: gfx950 takes unaligned global vector
+// accesses, so rows of any width and tensors that start anywhere in a buffer
+// use the same loads.
+template <int WORDS> struct WordsOf { typedef uint32_t type __attribute__((ext_vector_type(WORDS))); };
+template <> struct WordsOf<1> { typedef uint32_t type; };
 
-// Eight elements as loaded, kept raw until they are used (half the registers
-// for bf16).
-template <typename E> struct Eight;
+template <typename T, int ALIGN> struct Unaligned;
+template <typename T> struct Unaligned<T, 4> { typedef T type __attribute__((aligned(4))); };
+template <typename T> struct Unaligned<T, 2> { typedef T type __attribute__((aligned(2))); };
+template <typename T> struct Unaligned<T, 1> { typedef T type __attribute__((aligned(1))); };
 
-template <> struct Eight<float> {
-  u32x4_t q[2];
-  __device__ __forceinline__ void load(const float* p) {
-    q[0] = *reinterpret_cast<const u32x4_a4_t*>(p);
-    q[1] = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
-  }
-  __device__ __forceinline__ void load_part(const float* p, int n) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i >> 2][i & 3] = i < n ? __float_as_uint(p[i]) : 0u;
-  }
-  __device__ __forceinline__ float get(int i) const { return __uint_as_float(q[i >> 2][i & 3]); }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-    u32x4_t a, b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = __float_as_uint(v[i]);
-      b[i] = __float_as_uint(v[4 + i]);
+__device__ __forceinline__ uint32_t word_of(uint32_t w, int) { return w; }
+template <typename T> __device__ __forceinline__ uint32_t word_of(T w, int i) { return w[i]; }
+__device__ __forceinline__ void set_word(uint32_t& w, int, uint32_t v) { w = v; }
+template <typename T> __device__ __forceinline__ void set_word(T& w, int i, uint32_t v) { w[i] = v; }
+
+// V elements as they lie in memory.  STREAM: the access does not ask to stay
+// in the caches.
+template <typename E, int V>
+struct Pack {
+  static constexpr int kWords = V * int(sizeof(E)) / 4;
+  static constexpr int kPer = 4 / int(sizeof(E));  // elements of a word
+  static constexpr int kBits = 8 * int(sizeof(E));
+  typedef typename WordsOf<kWords>::type words_t;
+  typedef typename Unaligned<words_t, int(sizeof(E))>::type at_t;
+  words_t q;
+
+  __device__ __forceinline__ uint32_t word(int i) const { return word_of(q, i); }
+
+  // The first n of V elements, the others 0 (n <= 0 touches nothing).
+  template <bool STREAM = false>
+  __device__ __forceinline__ void load(const E* p, int n) {
+    if (n >= V) {
+      if constexpr (STREAM)
+        q = __builtin_nontemporal_load(reinterpret_cast<const at_t*>(p));
+      else
+        q = *reinterpret_cast<const at_t*>(p);
+      return;
     }
-    *reinterpret_cast<u32x4_a4_t*>(p) = a;
-    *reinterpret_cast<u32x4_a4_t*>(p + 4) = b;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (w * kPer + i < n) v |= bits_of(p[w * kPer + i]) << (kBits * i);
+      set_word(q, w, v);
+    }
   }
-};
 
-template <> struct Eight<uint16_t> {
-  u32x4_t q;
-  __device__ __forceinline__ void load(const uint16_t* p) {
-    q = *reinterpret_cast<const u32x4_a2_t*>(p);
-  }
-  __device__ __forceinline__ void load_part(const uint16_t* p, int n) {
-    uint32_t e[8];
+  template <bool STREAM = false>
+  __device__ __forceinline__ void store(E* p, int n) const {
+    if (n >= V) {
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(q, reinterpret_cast<at_t*>(p));
+      else
+        *reinterpret_cast<at_t*>(p) = q;
+      return;
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = e[2 * i] | (e[2 * i + 1] << 16);
+    for (int i = 0; i < V; ++i)
+      if (i < n) put_bits(p + i, word(i / kPer) >> (kBits * (i % kPer)));
   }
+
+  // As 32-bit floats (float and bf16).
   __device__ __forceinline__ float get(int i) const {
-    return (i & 1) ? bf16hi(q[i >> 1]) : bf16lo(q[i >> 1]);
+    if constexpr (sizeof(E) == 4) return __uint_as_float(word(i));
+    return (i & 1) ? bf16hi(word(i >> 1)) : bf16lo(word(i >> 1));
   }
-  static __device__ __forceinline__ void store(uint16_t* p, const float (&v)[8]) {
-    u32x4_t a;
+  __device__ __forceinline__ void set(const float (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<u32x4_a2_t*>(p) = a;
+    for (int w = 0; w < kWords; ++w) {
+      if constexpr (sizeof(E) == 4)
+        set_word(q, w, __float_as_uint(v[w]));
+      else
+        set_word(q, w, pack_bf16x2(v[2 * w], v[2 * w + 1]));
+    }
   }
+
+  static __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
+  static __device__ __forceinline__ uint32_t bits_of(uint16_t v) { return v; }
+  static __device__ __forceinline__ uint32_t bits_of(uint8_t v) { return v; }
+  static __device__ __forceinline__ void put_bits(float* p, uint32_t b) { *p = __uint_as_float(b); }
+  static __device__ __forceinline__ void put_bits(uint16_t* p, uint32_t b) { *p = uint16_t(b); }
+  static __device__ __forceinline__ void put_bits(uint8_t* p, uint32_t b) { *p = uint8_t(b); }
 };
 
-// The first n (at most 8) of eight elements; lanes with n <= 0 touch nothing.
-template <typename E>
-__device__ __forceinline__ void load_eight(Eight<E>& r, const E* p, int n) {
-  if (n >= 8)
-    r.load(p);
-  else
-    r.load_part(p, n);
-}
-
-template <typename E>
-__device__ __forceinline__ void store_eight(E* p, int n, const float (&v)[8]) {
-  if (n >= 8) {
-    Eight<E>::store(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) Elem<E>::st(p, i, v[i]);
-  }
+template <typename E, int V>
+__device__ __forceinline__ Pack<E, V> packed(const float (&v)[V]) {
+  Pack<E, V> r;
+  r.set(v);
+  return r;
 }
 
 // ---- e4m3 (OCP: 4 exponent bits, 3 mantissa bits, largest value 448) ----
@@ -90,13 +106,14 @@ __device__ __forceinline__ void store_eight(E* p, int n, const float (&v)[8]) {
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126: no scale is below it
 
-// Eight values of at most 448 in size to e4m3, round to nearest even.
-__device__ __forceinline__ u32x2_t pack_e4m3(const float (&v)[8]) {
-  u32x2_t r;
+// V values of at most 448 in size to e4m3, round to nearest even.
+template <int V>
+__device__ __forceinline__ Pack<uint8_t, V> pack_e4m3(const float (&v)[V]) {
+  Pack<uint8_t, V> r;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
-    r[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], w, true);
+  for (int i = 0; i < V / 4; ++i) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+    set_word(r.q, i, __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], w, true));
   }
   return r;
 }
@@ -108,78 +125,48 @@ __device__ __forceinline__ u32x2_t pack_e4m3(const float (&v)[8]) {
 // (compared with the formula on four million values); it replaces eleven
 // operations an element.  A |v| that its scaling left a few units above 448
 // stays at 448: the carry into the next step needs more than 15 units.
-__device__ __forceinline__ u32x2_t pack_e4m3_stochastic(const float (&v)[8], const uint32_t (&rnd)[8]) {
-  u32x2_t r;
+template <int V>
+__device__ __forceinline__ Pack<uint8_t, V> pack_e4m3_stochastic(const float (&v)[V],
+                                                                 const uint32_t (&rnd)[V]) {
+  Pack<uint8_t, V> r;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < V / 4; ++i) {
     int w = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i], rnd[4 * i], 0, 0);
     w = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i + 1], rnd[4 * i + 1], w, 1);
     w = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i + 2], rnd[4 * i + 2], w, 2);
-    r[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i + 3], rnd[4 * i + 3], w, 3);
+    set_word(r.q, i, __builtin_amdgcn_cvt_sr_fp8_f32(v[4 * i + 3], rnd[4 * i + 3], w, 3));
   }
   return r;
 }
 
 // 32 bits to bf16 in the same way (v_cvt_sr_bf16_f32; NaN stays NaN).
-__device__ __forceinline__ u32x4_t pack_bf16_stochastic(const float (&v)[8], const uint32_t (&rnd)[8]) {
-  u32x4_t r;
+template <int V>
+__device__ __forceinline__ Pack<uint16_t, V> pack_bf16_stochastic(const float (&v)[V],
+                                                                  const uint32_t (&rnd)[V]) {
+  Pack<uint16_t, V> r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < V / 2; ++i) {
     bf16x2_t w = {};
     w = __builtin_amdgcn_cvt_sr_bf16_f32(w, v[2 * i], rnd[2 * i], false);
     w = __builtin_amdgcn_cvt_sr_bf16_f32(w, v[2 * i + 1], rnd[2 * i + 1], true);
-    r[i] = __builtin_bit_cast(uint32_t, w);
+    set_word(r.q, i, __builtin_bit_cast(uint32_t, w));
   }
   return r;
 }
 
-// The first n of eight packed elements.
-__device__ __forceinline__ void store_packed(uint8_t* p, int n, u32x2_t r) {
-  if (n >= 8) {
-    *reinterpret_cast<u32x2_a1_t*>(p) = r;
-  } else {
+// e4m3 codes as 32-bit floats.
+template <int V>
+__device__ __forceinline__ void unpack_e4m3(const Pack<uint8_t, V>& r, float (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = static_cast<uint8_t>(r[i >> 2] >> (8 * (i & 3)));
+  for (int i = 0; i < V / 4; ++i) {
+    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(r.word(i), false);
+    const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8(r.word(i), true);
+    v[4 * i] = a[0];
+    v[4 * i + 1] = a[1];
+    v[4 * i + 2] = b[0];
+    v[4 * i + 3] = b[1];
   }
 }
-
-__device__ __forceinline__ void store_packed(uint16_t* p, int n, u32x4_t r) {
-  if (n >= 8) {
-    *reinterpret_cast<u32x4_a2_t*>(p) = r;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = static_cast<uint16_t>(r[i >> 1] >> (16 * (i & 1)));
-  }
-}
-
-struct EightE4m3 {
-  u32x2_t q;
-  __device__ __forceinline__ void load(const uint8_t* p, int n) {
-    if (n >= 8) {
-      q = *reinterpret_cast<const u32x2_a1_t*>(p);
-    } else {
-      uint32_t e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : 0u;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        q[i] = e[4 * i] | (e[4 * i + 1] << 8) | (e[4 * i + 2] << 16) | (e[4 * i + 3] << 24);
-    }
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(q[i], false);
-      const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8(q[i], true);
-      v[4 * i] = a[0];
-      v[4 * i + 1] = a[1];
-      v[4 * i + 2] = b[0];
-      v[4 * i + 3] = b[1];
-    }
-  }
-};
 
 // ---- reductions over lanes ----
 
@@ -214,20 +201,22 @@ __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b 
 // infinity and is not lost.
 __device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Maximum over groups of LANES (4, 8 or 16) consecutive lanes.
+// Maximum over groups of LANES (4, 8, 16 or 32) consecutive lanes.
 template <int LANES>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   v = umax(v, dpp<kDppXor1>(v));
   v = umax(v, dpp<kDppXor2>(v));
   if constexpr (LANES >= 8) v = umax(v, dpp<kDppHalfMirror>(v));
   if constexpr (LANES >= 16) v = umax(v, dpp<kDppMirror>(v));
+  if constexpr (LANES >= 32) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = umax(a[0], a[1]);
+  }
   return v;
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = group_max<16>(v);
-  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = umax(a[0], a[1]);
+  v = group_max<32>(v);
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return umax(b[0], b[1]);
 }
