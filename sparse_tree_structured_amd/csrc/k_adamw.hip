@@ -73,6 +73,38 @@ struct Quad {
   f32x2_t scale;
 };
 
+// Correctly rounded square root and quotient by an approximation, its error
+// by fma and one correction (Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", 1990): 40 and 36 cycles of a
+// wavefront where the compiler's, which also serve operands near the ends of
+// the range, take 76 and 52; the 8-bit step is bound by them.  For v = 0 and
+// v in [2^-90, 2^60) the root is the IEEE one for every mantissa (all were
+// compared); the quotient for m = 0 and m in [2^-60, 2^60) over
+// [2^-60, 2^90) (4e9 pairs compared).
+__device__ __forceinline__ float short_sqrt(float v) {
+#pragma clang fp contract(off)
+  const float y = __builtin_amdgcn_rsqf(v);
+  const float g = v * y;
+  const float s = __builtin_fmaf(__builtin_fmaf(-g, g, v), 0.5f * y, g);
+  return v == 0.0f ? v : s;
+}
+
+__device__ __forceinline__ float short_div(float m, float d) {
+#pragma clang fp contract(off)
+  float y = __builtin_amdgcn_rcpf(d);
+  y = __builtin_fmaf(__builtin_fmaf(-d, y, 1.0f), y, y);
+  const float q = m * y;
+  return __builtin_fmaf(__builtin_fmaf(-q, d, m), y, q);
+}
+
+// The ranges' ends: 2 bits(m) - 1 and bits(v) - 1 (zero wraps to the top).
+constexpr uint32_t kShortLowM = 2 * (67u << 23) - 1;  // 2^-60
+constexpr uint32_t kShortLowV = (37u << 23) - 1;      // 2^-90
+constexpr float kShortTop = 0x1p60f;
+constexpr float kShortEps = 0x1p-60f;
+
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
 // One chunk of one tensor (FULL: all of it inside the tensor, which then
 // needs no tests for the end).  A lane's quads are kThreads * kV apart, so
 // that every access of a wavefront is contiguous; all are loaded before the
@@ -127,18 +159,36 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
         r[i] = q[k].v.get(i);
       }
     }
-    uint32_t top_m = 0, top_r = 0;
+    // m / denominator and sqrt(v) in the short forms where every operand of
+    // this lane is zero or in their range, which is all but always.
+    float v[kV], ratio[kV];
+    uint32_t low_m = ~0u, low_v = ~0u;  // smallest sizes above zero, zero as the largest
+    float top_m = 0.0f, top_r = 0.0f, top_v = 0.0f;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const float g = q[k].g.get(i) * gs;
       m[i] = m[i] * a.beta1 + g * a.one_beta1;
-      const float v = r[i] * a.beta2 + (g * g) * a.one_beta2;
-      const float root = sqrtf(v);
-      w[i] = q[k].p.get(i) * t.decay - t.step * (m[i] / (root * a.root + a.eps));
-      r[i] = E4M3 ? root : v;
-      top_m = umax(top_m, size_bits(m[i]));
-      top_r = umax(top_r, __float_as_uint(root));  // root >= 0, or NaN
+      v[i] = r[i] * a.beta2 + (g * g) * a.one_beta2;
+      r[i] = short_sqrt(v[i]);
+      ratio[i] = short_div(m[i], r[i] * a.root + a.eps);
+      low_m = umin(low_m, 2 * __float_as_uint(m[i]) - 1);
+      low_v = umin(low_v, __float_as_uint(v[i]) - 1);
+      top_m = fmaxf(top_m, fabsf(m[i]));
+      top_r = fmaxf(top_r, r[i]);
+      top_v = fmaxf(top_v, v[i]);
     }
+    if (low_m < kShortLowM || low_v < kShortLowV || !(top_m < kShortTop && top_v < kShortTop) ||
+        a.eps < kShortEps) {
+      top_r = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        r[i] = sqrtf(v[i]);
+        ratio[i] = m[i] / (r[i] * a.root + a.eps);
+        top_r = fmaxf(top_r, r[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) w[i] = q[k].p.get(i) * t.decay - t.step * ratio[i];
     uint32_t h[kV], rnd[kV];
     if constexpr (STOCHASTIC) {
       const uint32_t base = t.key ^ (static_cast<uint32_t>(i0 >> 32) * 0x9E3779B9u);
@@ -156,15 +206,15 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
     }
     if constexpr (!E4M3) {
       packed<float, kV>(m).template store<STREAM>(ms + i0, n);
-      packed<float, kV>(r).template store<STREAM>(vs + i0, n);
+      packed<float, kV>(v).template store<STREAM>(vs + i0, n);
       continue;
     }
     // The block's 32 lanes are two rows of 16.  One swap of the rows leaves
     // both maxima of m in the first row and both of r in the second, so that
     // one division serves both scales; another gives every lane both.
     // Lanes past the tensor's end hold zeros, which no maximum sees.
-    const auto top = __builtin_amdgcn_permlane16_swap(group_max<16>(top_m), group_max<16>(top_r),
-                                                      false, false);
+    const auto top = __builtin_amdgcn_permlane16_swap(
+        group_max<16>(__float_as_uint(top_m)), group_max<16>(__float_as_uint(top_r)), false, false);
     const float scale = e4m3_scale(umax(top[0], top[1]));
     const float inv = 1.0f / scale;
     const auto both = __builtin_amdgcn_permlane16_swap(__float_as_uint(inv), __float_as_uint(inv),
@@ -174,8 +224,8 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
     for (int i = 0; i < kV; ++i) {
       m[i] *= im;
       r[i] *= ir;
-      // at least the smallest code, which every rounding of it keeps
-      r[i] = r[i] > 0.0f ? fmaxf(r[i], 0.001953125f) : r[i];
+      // above zero, at least the smallest code, which every rounding keeps
+      r[i] = r[i] > 0.0f ? fmaxf(r[i], 0x1p-9f) : r[i];
     }
     Pack<uint8_t, kV> qm, qr;
     if constexpr (STOCHASTIC) {

@@ -65,9 +65,11 @@ struct AdamwEntry {
     lo[which] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
     hi[which] = static_cast<uint16_t>(reinterpret_cast<uintptr_t>(p) >> 32);
   }
-  template <typename T> __host__ __device__ T* get(int which) const {
-    return reinterpret_cast<T*>(static_cast<uintptr_t>(lo[which]) |
-                                static_cast<uintptr_t>(hi[which]) << 32);
+  // By way of a global pointer, or the compiler takes the accesses for
+  // flat ones.
+  template <typename T> __device__ T* get(int which) const {
+    return (T*)(__attribute__((address_space(1))) T*)(
+        static_cast<uintptr_t>(lo[which]) | static_cast<uintptr_t>(hi[which]) << 32);
   }
 };
 constexpr int kAddressBits = 48;

@@ -184,6 +184,49 @@ def test_a_moment_keeps_its_mean_and_stays_above_zero():
     assert (v[0].float()[1::128] == 2.0 ** -9).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_nan_stays_with_its_element_and_infinity_is_not_lost(bits):
+    """No clipping in front: a NaN gradient makes its own element NaN and
+    leaves the rest of its block as it would be; an infinite one is NaN or
+    infinite in its element."""
+    rng = np.random.default_rng(12)
+    w = rng.normal(size=300).astype(np.float32)
+    g = rng.normal(size=300).astype(np.float32)
+    out = {}
+    for bad in (0.0, float("nan"), float("inf")):
+        p, gg = dev(w), dev(g)
+        gg[70] = bad
+        m, v, s = fff.adamw_state([p], bits=bits)
+        table = fff.adamw_table([p], [gg], m, v, scales=s)
+        for step in (1, 2):
+            fff.adamw_step(table, step=step, seed=step, **KW)
+        out[str(bad)] = [f32(p), f32(m[0]), f32(v[0])]
+    for a, b in zip(out["0.0"], out["nan"]):
+        assert np.isnan(b[70]) and np.array_equal(np.delete(a, 70), np.delete(b, 70))
+    p, m, v = out["inf"]
+    assert not np.isfinite(p[70]) and np.isfinite(p[[0, 127]] if bits == 32 else p[128:]).all()
+
+
+def test_sizes_beyond_the_short_forms():
+    """Moments whose sizes need the long division and root: bit for bit."""
+    rng = np.random.default_rng(13)
+    n = 4096
+    size = 2.0 ** rng.uniform(-140, 120, n)
+    size[rng.random(n) < 0.1] = 0.0
+    for eps in (1e-8, 0.0, 1e-30):
+        kw = dict(KW, eps=eps)
+        p, g = rng.normal(size=n).astype(np.float32), (rng.normal(size=n) * size).astype(np.float32)
+        m = (g * rng.normal(size=n)).astype(np.float32)
+        with np.errstate(over="ignore", under="ignore", invalid="ignore", divide="ignore"):
+            v = np.minimum((g * g).astype(np.float32) * rng.random(n).astype(np.float32), 1e38).astype(np.float32)
+            o = O.adamw(p, g, m, v, wd=0.0, step=3, **kw)
+        t = [dev(a) for a in (p, g, m, v)]
+        fff.adamw_step(fff.adamw_table([t[0]], [t[1]], [t[2]], [t[3]]), step=3, **kw)
+        same(f32(t[0]), o["p"], f"param, eps {eps}")
+        same(f32(t[2]), o["m"], f"exp_avg, eps {eps}")
+        same(f32(t[3]), o["v"], f"exp_avg_sq, eps {eps}")
+
+
 def test_elements_past_32_bits():
     """A tensor of more than 2^32 elements: offsets, blocks and random
     numbers of its last elements."""
