@@ -16,6 +16,7 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;
 // Workgroups of one launch: 256 threads each, and a launch has fewer than
 // 2^32 threads.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
+static_assert(fff::kNormSmallChunks <= fff::kNormMaxTensors, "a small list fits the arguments");
 // One tensor of the optimiser fits one launch.
 constexpr int64_t kMaxTensor = int64_t(1) << 34;
 static_assert(kMaxTensor / fff::kAdamwChunk <= kMaxBlocks &&
@@ -79,11 +80,21 @@ fff_status_t check_grads(const fff_adamw_tensor_t* tensors, int64_t count) {
   return FFF_SUCCESS;
 }
 
-int64_t grad_chunks(const fff_adamw_tensor_t* tensors, int64_t count) {
+int64_t grad_chunks(const fff_adamw_tensor_t* tensors, int64_t count, int chunk) {
   int64_t n = 0;
-  for (int64_t i = 0; i < count; ++i)
-    n += (tensors[i].n + fff::kNormChunk - 1) / fff::kNormChunk;
+  for (int64_t i = 0; i < count; ++i) n += (tensors[i].n + chunk - 1) / chunk;
   return n;
+}
+
+// Whether one workgroup takes all of the list.
+bool grads_small(const fff_adamw_tensor_t* tensors, int64_t count) {
+  return grad_chunks(tensors, count, fff::kNormSmallChunk) <= fff::kNormSmallChunks;
+}
+
+size_t grad_norm_bytes(const fff_adamw_tensor_t* tensors, int64_t count) {
+  return grads_small(tensors, count)
+             ? 0
+             : size_t(grad_chunks(tensors, count, fff::kNormChunk)) * sizeof(double);
 }
 
 }  // namespace
@@ -261,7 +272,7 @@ fff_status_t fff_grad_norm_workspace_size(const fff_adamw_tensor_t* tensors, int
   fff_status_t st = check_grads(tensors, count);
   if (st != FFF_SUCCESS) return st;
   if (!bytes) return FFF_ERROR_INVALID_VALUE;
-  *bytes = size_t(grad_chunks(tensors, count)) * sizeof(double);
+  *bytes = grad_norm_bytes(tensors, count);
   return FFF_SUCCESS;
 }
 
@@ -271,11 +282,11 @@ fff_status_t fff_grad_norm(const fff_adamw_tensor_t* tensors, int64_t count, dou
   fff_status_t st = check_grads(tensors, count);
   if (st != FFF_SUCCESS) return st;
   if (!(max_norm > 0.0) || !good(out, FFF_DTYPE_F32)) return FFF_ERROR_INVALID_VALUE;
-  const int64_t chunks = grad_chunks(tensors, count);
-  if (chunks > 0) {
-    if (!workspace || workspace_bytes < size_t(chunks) * sizeof(double)) return FFF_ERROR_WORKSPACE;
-    if (!aligned(workspace, 256)) return FFF_ERROR_INVALID_VALUE;
-  }
+  const size_t need_bytes = grad_norm_bytes(tensors, count);
+  if (need_bytes > 0 && (!workspace || workspace_bytes < need_bytes)) return FFF_ERROR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FFF_ERROR_INVALID_VALUE;
+  const bool small = grads_small(tensors, count);
+  const int chunk = small ? fff::kNormSmallChunk : fff::kNormChunk;
   double* partial = static_cast<double*>(workspace);
   fff::GradNormArgs a;
   int64_t blocks = 0, done = 0;
@@ -292,7 +303,7 @@ fff_status_t fff_grad_norm(const fff_adamw_tensor_t* tensors, int64_t count, dou
   for (int64_t i = 0; i < count; ++i) {
     const fff_adamw_tensor_t& t = tensors[i];
     if (t.n == 0) continue;
-    const int64_t need = (t.n + fff::kNormChunk - 1) / fff::kNormChunk;
+    const int64_t need = (t.n + chunk - 1) / chunk;
     if ((a.count == fff::kNormMaxTensors || blocks + need > kMaxBlocks) && flush() != hipSuccess)
       return FFF_ERROR_HIP;
     a.first[a.count] = static_cast<uint32_t>(blocks);
@@ -301,8 +312,11 @@ fff_status_t fff_grad_norm(const fff_adamw_tensor_t* tensors, int64_t count, dou
     e.n = t.grad_dtype == FFF_DTYPE_BF16 ? -t.n : t.n;
     blocks += need;
   }
+  if (small)  // at most one tensor to a chunk: the list fits the arguments
+    return hip_status(fff::launch_grad_norm_small(a, static_cast<uint32_t>(blocks), max_norm, out,
+                                                  stream));
   if (flush() != hipSuccess) return FFF_ERROR_HIP;
-  return hip_status(fff::launch_grad_norm_final(partial, chunks, max_norm, out, stream));
+  return hip_status(fff::launch_grad_norm_final(partial, done, max_norm, out, stream));
 }
 
 }  // extern "C"

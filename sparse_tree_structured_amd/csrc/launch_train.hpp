@@ -90,7 +90,9 @@ enum AdamwParam { kParamF32 = 0, kParamBf16 = 1, kParamMaster = 2 };
 hipError_t launch_adamw(const AdamwArgs& a, int blocks, int param, bool grad_bf16, bool state_e4m3,
                         bool stochastic, hipStream_t st);
 
-constexpr int kNormChunk = 16384;   // gradient elements per workgroup
+constexpr int kNormChunk = 16384;     // gradient elements per workgroup
+constexpr int kNormSmallChunk = 1024;  // per wavefront, for a small list
+constexpr int kNormSmallChunks = 64;   // of at most so many of these
 constexpr int kNormMaxTensors = 192;
 
 struct GradEntry {
@@ -107,6 +109,8 @@ struct GradNormArgs {
 static_assert(sizeof(GradNormArgs) <= 4096, "kernel arguments");
 
 hipError_t launch_grad_squares(const GradNormArgs& a, int blocks, hipStream_t st);
+hipError_t launch_grad_norm_small(const GradNormArgs& a, uint32_t chunks, double max_norm, float* out,
+                                  hipStream_t st);
 hipError_t launch_grad_norm_final(const double* partial, int64_t count, double max_norm, float* out,
                                   hipStream_t st);
 
