@@ -66,9 +66,14 @@ struct Pack {
         *reinterpret_cast<at_t*>(p) = q;
       return;
     }
+    store_range(p, 0, n);
+  }
+
+  // Elements lo .. hi - 1 of the V at p.
+  __device__ __forceinline__ void store_range(E* p, int lo, int hi) const {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < n) put_bits(p + i, word(i / kPer) >> (kBits * (i % kPer)));
+      if (i >= lo && i < hi) put_bits(p + i, word(i / kPer) >> (kBits * (i % kPer)));
   }
 
   // As 32-bit floats (float and bf16).

@@ -154,6 +154,25 @@ def test_in_place_and_views():
         assert buf[0] == 0 and (buf[1 + T * d:3 + T * d] == 0).all() and (buf[3 + 2 * T * d:] == 0).all()
 
 
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [5, 257, 513, 769, 1025, 1030, 2051, 4097])
+def test_in_place_at_ragged_ends(d, ty):
+    """Widths whose last columns start another wavefront's or chunk's access,
+    so that two of them hold some columns: in place gives the same bits."""
+    T = 2000
+    x, r, w = inputs(T, d, ty, ty, seed=4)
+    want = fff.rms_norm(x, w, residual=r, want_rstd=True)
+    dres = randn(np.random.default_rng(d), (T, d), ty)
+    grad = fff.rms_norm_backward(x, want.residual_out, w, want.rstd, dresidual=dres)
+    print(f"[gpu] in place d={d} {ty}", flush=True)
+    for _ in range(3):
+        a, b, c = x.clone(), r.clone(), dres.clone()
+        o = fff.rms_norm(a, w, residual=b, residual_out=b, y=a, want_rstd=True)
+        assert torch.equal(a, want.y) and torch.equal(b, want.residual_out) and torch.equal(o.rstd, want.rstd)
+        g = fff.rms_norm_backward(x, b, w, o.rstd, dresidual=c, dz=c)
+        assert torch.equal(c, grad.dz) and torch.equal(g.dweight, grad.dweight)
+
+
 @pytest.mark.parametrize("ty,st", PAIRS)
 @pytest.mark.parametrize("T,d", [(1, 1), (1, 2048), (3, 70), (50, 512), (17, 513), (1030, 100),
                                  (700, 767), (1500, 2048), (40, 3001), (5, 8192), (3, 8200),
