@@ -614,10 +614,10 @@ def _here(t, stream):
     """The handle of the stream to launch on: `stream`, or the current one.
     The library launches on the current device, so tensors must be there."""
     torch = _torch()
-    if not t.is_cuda:
-        raise ValueError(f"tensors must be on a GPU, not {t.device}")
     index = t.get_device()
-    if index != torch.cuda.current_device():
+    if index < 0:
+        raise ValueError(f"tensors must be on a GPU, not {t.device}")
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on {t.device}, which is not the current device")
     if stream is not None:
         return int(stream.cuda_stream)
@@ -636,15 +636,15 @@ def _empty(shape, dtype, device, stream):
 def _tensor(t, shape, dtype, device, what):
     """The pointer of a tensor that must have this shape, dtype and device
     and be contiguous."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous")
 
 
 def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset: float = 0.0,
@@ -889,6 +889,9 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
         if e4m3:
             e.scale = _flat(sc, 2 * -(-e.n // ADAMW_BLOCK), f32, dev, f"scales[{i}]")
         e.lr_scale, e.weight_decay = float(shares[i]), float(decays[i])
+    written = [q for e in entries if e.n for q in (e.param, e.master, e.exp_avg, e.exp_avg_sq) if q]
+    if len(set(written)) != len(written):
+        raise ValueError("a tensor is in the table twice: every param, master and state must be its own")
     return TensorTable(entries, params[0], DTYPE_E4M3 if e4m3 else DTYPE_F32, (params, lists))
 
 

@@ -75,18 +75,17 @@ struct Quad {
 
 // Correctly rounded square root and quotient by an approximation, its error
 // by fma and one correction (Markstein, "Computation of elementary functions
-// on the IBM RISC System/6000 processor", 1990): 40 and 36 cycles of a
-// wavefront where the compiler's, which also serve operands near the ends of
-// the range, take 76 and 52; the 8-bit step is bound by them.  For v = 0 and
-// v in [2^-90, 2^60) the root is the IEEE one for every mantissa (all were
-// compared); the quotient for m = 0 and m in [2^-60, 2^60) over
-// [2^-60, 2^90) (4e9 pairs compared).
+// on the IBM RISC System/6000 processor", 1990): 36 cycles of a wavefront
+// each where the compiler's, which also serve operands near the ends of the
+// range, take 76 and 52; the 8-bit step is bound by them.  The root is the
+// IEEE one for v = 0 and every v in [2^-90, 2^60) (all compared); the
+// quotient for m = 0 and m in [2^-60, 2^60) over [2^-60, 2^90) (4e9 pairs
+// compared).
 __device__ __forceinline__ float short_sqrt(float v) {
 #pragma clang fp contract(off)
-  const float y = __builtin_amdgcn_rsqf(v);
+  const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));  // (finite for v = 0)
   const float g = v * y;
-  const float s = __builtin_fmaf(__builtin_fmaf(-g, g, v), 0.5f * y, g);
-  return v == 0.0f ? v : s;
+  return __builtin_fmaf(__builtin_fmaf(-g, g, v), 0.5f * y, g);
 }
 
 __device__ __forceinline__ float short_div(float m, float d) {
@@ -216,7 +215,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
     const auto top = __builtin_amdgcn_permlane16_swap(
         group_max<16>(__float_as_uint(top_m)), group_max<16>(__float_as_uint(top_r)), false, false);
     const float scale = e4m3_scale(umax(top[0], top[1]));
-    const float inv = 1.0f / scale;
+    const float inv = reciprocal(scale);
     const auto both = __builtin_amdgcn_permlane16_swap(__float_as_uint(inv), __float_as_uint(inv),
                                                        false, false);
     const float im = __uint_as_float(both[0]), ir = __uint_as_float(both[1]);

@@ -209,7 +209,7 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
         const int col = (c * kTeam + lane) * V;
         if (a.group != 0) top[c] = group_top<V>(top[c], a.group);
         const float scale = e4m3_scale(top[c]);
-        const float inv = 1.0f / scale;
+        const float inv = reciprocal(scale);
 #pragma unroll
         for (int i = 0; i < V; ++i) z[c][i] *= inv;
         if (col < a.d) {

@@ -232,4 +232,14 @@ __device__ __forceinline__ float e4m3_scale(uint32_t bits) {
   return s < kTinyScale ? kTinyScale : s;
 }
 
+// 1 / s for a scale, correctly rounded: an approximation and one correction
+// by fma (equal to the IEEE quotient for every s from 2^-126 to 2^120; a
+// scale is at most 2^128 / 448, or infinite).
+__device__ __forceinline__ float reciprocal(float s) {
+#pragma clang fp contract(off)
+  const float y = __builtin_amdgcn_rcpf(s);
+  const float r = __builtin_fmaf(__builtin_fmaf(-s, y, 1.0f), y, y);
+  return __builtin_isinf(s) ? 0.0f : r;
+}
+
 }  // namespace fff

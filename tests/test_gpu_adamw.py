@@ -227,6 +227,44 @@ def test_sizes_beyond_the_short_forms():
         same(f32(t[3]), o["v"], f"exp_avg_sq, eps {eps}")
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_large_lists_read_past_the_caches(bits):
+    """A list large enough for streaming accesses, its tensors at odd
+    elements, against the same tensors a few at a time."""
+    sizes = [4_000_001, 3_000_127, 5, 2_500_000]  # 30 or 18 bytes an element
+    sizes = sizes + ([] if bits == 32 else [3_000_003])
+    state = []
+    for n in sizes:
+        buf = {"w": torch.empty(n + 1, device=DEV)[1:], "g": torch.empty(n + 3, device=DEV)[3:],
+               "p": torch.empty(n + 1, device=DEV, dtype=torch.bfloat16)[1:]}
+        buf["w"].normal_()
+        buf["g"].normal_()
+        buf["p"].copy_(buf["w"])
+        buf["m"], buf["v"] = (torch.zeros(n + 1, dtype=torch.float32 if bits == 32 else torch.uint8, device=DEV)[1:]
+                              for _ in range(2))
+        if bits == 8:
+            buf["m"], buf["v"] = buf["m"].view(F8), buf["v"].view(F8)
+            buf["s"] = torch.zeros(-(-n // 128), 2, device=DEV)
+        state.append(buf)
+    other = [{k: v.clone() for k, v in b.items()} for b in state]
+
+    def table(bs):
+        return fff.adamw_table([b["p"] for b in bs], [b["g"] for b in bs], [b["m"] for b in bs], [b["v"] for b in bs],
+                               masters=[b["w"] for b in bs], scales=[b["s"] for b in bs] if bits == 8 else None)
+
+    for step in (1, 2):
+        fff.adamw_step(table(state), step=step, **KW)
+        for b in other:
+            fff.adamw_step(table([b]), step=step, **KW)
+    for a, b in zip(state, other):
+        for k in a:
+            assert torch.equal(a[k].view(torch.uint8) if a[k].dtype == F8 else a[k],
+                               b[k].view(torch.uint8) if b[k].dtype == F8 else b[k]), k
+    big = torch.randn(44_000_003, device=DEV)[1:]  # 176 MB
+    want = float(big.double().square().sum().sqrt())
+    assert abs(float(fff.grad_norm([big])[0]) - want) <= 1.01 * O.U32 * want
+
+
 def test_elements_past_32_bits():
     """A tensor of more than 2^32 elements: offsets, blocks and random
     numbers of its last elements."""
