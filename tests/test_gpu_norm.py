@@ -234,6 +234,30 @@ def test_backward_in_place_without_dweight_and_same_every_time():
     assert torch.equal(first.dz, into)
 
 
+@pytest.mark.parametrize("mb", [100, 260])
+@pytest.mark.parametrize("ty,st,d", [("bf16", "bf16", 4099), ("bf16", "bf16", 4096), ("bf16", "f32", 2051),
+                                     ("f32", "f32", 2048)])
+@pytest.mark.parametrize("out", [None, F8])
+def test_forward_of_large_batches_past_the_caches(mb, ty, st, d, out):
+    """A batch large enough for streaming writes, and reads, against its rows
+    a part at a time (which are not)."""
+    T = (mb << 20) // (d * ((4 if ty == "f32" else 2) * (1 if out else 2) + 2 * (4 if st == "f32" else 2)))
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(d)
+    x = torch.randn(T, d, generator=gen, device=DEV).to(TY[ty])
+    r = torch.randn(T, d, generator=gen, device=DEV).to(TY[st])
+    w = torch.randn(d, generator=gen, device=DEV).to(TY[ty])
+    kw = dict(out_dtype=out, group=64 if out else 0, want_rstd=True)
+    print(f"[gpu] rms_norm large T={T} d={d} {ty} {st} {out}", flush=True)
+    o = fff.rms_norm(x, w, residual=r, **kw)
+    n = T // 8 + 1
+    for a in range(0, T, n):
+        part = fff.rms_norm(x[a:a + n], w, residual=r[a:a + n], **kw)
+        assert torch.equal(o.y[a:a + n].view(torch.uint8), part.y.view(torch.uint8))
+        assert torch.equal(o.residual_out[a:a + n], part.residual_out) and torch.equal(o.rstd[a:a + n], part.rstd)
+        assert out is None or torch.equal(o.scale[a:a + n], part.scale)
+
+
 @pytest.mark.parametrize("ty,st,d", [("bf16", "bf16", 4099), ("bf16", "bf16", 4096), ("f32", "f32", 2051)])
 def test_backward_of_large_batches_past_the_caches(ty, st, d):
     """A batch large enough for streaming reads against its rows a part at a
