@@ -472,7 +472,8 @@ fff_status_t fff_rms_norm(const fff_norm_shape_t *shape, const void *x, const vo
  *   dweight    [d] float32 out, or NULL
  * Rows are summed in a fixed order: results are the same on every call.  dz
  * and dx may be the buffers of inputs of their types.  T = 0 gives dweight 0.
- * The workspace is for dweight: without it, it may be NULL.
+ * The workspace is for dweight: without it, or where its size is 0 (small
+ * batches), it may be NULL.
  */
 fff_status_t fff_rms_norm_backward_workspace_size(const fff_norm_shape_t *shape, size_t *bytes);
 fff_status_t fff_rms_norm_backward(const fff_norm_shape_t *shape, const void *dy, const void *z,

@@ -769,8 +769,9 @@ def rms_norm_backward(dy, z, weight, rstd, *, dresidual=None, weight_offset: flo
         pws = _tensor(workspace, (have,), torch.uint8, dev, "workspace")
     elif dweight is not None:
         have = rms_norm_backward_workspace_size(T, d, code, zcode)
-        workspace = _empty((have,), torch.uint8, dev, stream)
-        pws = workspace.data_ptr()
+        if have:
+            workspace = _empty((have,), torch.uint8, dev, stream)
+            pws = workspace.data_ptr()
     st = load_library().fff_rms_norm_backward(
         _norm_shape(T, d, code, zcode, code, 0, 0.0, weight_offset), pdy, pz, pw, pr, pe, pdz, pdx,
         pdw, pws, have, handle)

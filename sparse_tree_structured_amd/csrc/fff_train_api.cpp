@@ -160,7 +160,7 @@ fff_status_t fff_rms_norm_backward(const fff_norm_shape_t* shape, const void* dy
         !good(rstd, FFF_DTYPE_F32) || !good_or_null(dresidual, s.stream_dtype) ||
         !good(dz, s.stream_dtype) || !good_or_null(dx, s.dtype))
       return FFF_ERROR_INVALID_VALUE;
-    if (dweight && (!workspace || workspace_bytes < need)) return FFF_ERROR_WORKSPACE;
+    if (dweight && need > 0 && (!workspace || workspace_bytes < need)) return FFF_ERROR_WORKSPACE;
     if (!aligned(workspace, 256)) return FFF_ERROR_INVALID_VALUE;
   }
   if (s.T == 0 && !dweight) return FFF_SUCCESS;
@@ -178,7 +178,7 @@ fff_status_t fff_rms_norm_backward(const fff_norm_shape_t* shape, const void* dy
   a.dz = dz;
   a.dx = dx;
   a.dweight = dweight;
-  a.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+  a.partial = dweight && need > 0 ? static_cast<float*>(workspace) : nullptr;
   return hip_status(fff::launch_rms_norm_backward(a, stream));
 }
 

@@ -165,6 +165,89 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void rms_norm_dweight_kernel
   }
 }
 
+// Small batches in one launch, without a workspace: the first a.rows (T, or
+// none) workgroups have a row of dz each, and the others 32 columns of dw, for
+// which they read dy and z once more (dw needs no row's dot).
+constexpr int kSmallThreads = 256, kSmallCols = 32;
+
+template <typename X, typename S, bool RAGGED, int C>
+__global__ __launch_bounds__(kSmallThreads) void rms_norm_backward_small_kernel(NormGradArgs a) {
+  constexpr int V = kCols<X, S>;
+  const X* dy = static_cast<const X*>(a.dy);
+  const S* zin = static_cast<const S*>(a.z);
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  if (static_cast<int>(blockIdx.x) < a.rows) {
+    using At = Span<V, RAGGED>;
+    __shared__ float lds[kSmallThreads / kWave];
+    const X* w = static_cast<const X*>(a.weight);
+    const S* dres = static_cast<const S*>(a.dresidual);
+    S* dz = static_cast<S*>(a.dz);
+    X* dx = static_cast<X*>(a.dx);
+    const size_t row = static_cast<size_t>(blockIdx.x) * a.d;
+    const float offset = a.weight_offset + (w ? 0.0f : 1.0f);
+    const float rstd = a.rstd[blockIdx.x];
+    Pack<X, V> yr[C], wr[C] = {};
+    Pack<S, V> zr[C], er[C] = {};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const At at((c * kSmallThreads + threadIdx.x) * V, a.d);
+      at.template load<false>(yr[c], dy + row);
+      at.template load<false>(zr[c], zin + row);
+      if (w) at.template load<false>(wr[c], w);
+      if (dres) at.template load<false>(er[c], dres + row);
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float g[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = yr[c].get(i) * (wr[c].get(i) + offset);
+      At((c * kSmallThreads + threadIdx.x) * V, a.d).clear(g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) dot += g[i] * (zr[c].get(i) * rstd);
+    }
+    dot = team_total<kSmallThreads / kWave>(dot, lds) * inv_d;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const At at((c * kSmallThreads + threadIdx.x) * V, a.d);
+      float v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        v[i] = rstd * (yr[c].get(i) * (wr[c].get(i) + offset) - zr[c].get(i) * rstd * dot) + er[c].get(i);
+      at.store(packed<S, V>(v), dz + row);
+      if (dx) at.store(packed<X, V>(v), dx + row);
+    }
+    return;
+  }
+  // 32 slices of the rows by eight lanes of four columns.
+  constexpr int kLanes = kSmallCols / 4, kSlices = kSmallThreads / kLanes;
+  __shared__ float sums[kSlices][kSmallCols + 1];
+  const int lane = threadIdx.x % kLanes, slice = threadIdx.x / kLanes;
+  const int first = (static_cast<int>(blockIdx.x) - a.rows) * kSmallCols;
+  const int col = first + lane * 4;
+  float s[4] = {};
+#pragma unroll 4
+  for (int64_t t = slice; t < a.T; t += kSlices) {
+    Pack<X, 4> y;
+    Pack<S, 4> z;
+    y.load(dy + t * a.d + col, a.d - col);
+    z.load(zin + t * a.d + col, a.d - col);
+    const float rstd = a.rstd[t];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] += y.get(i) * (z.get(i) * rstd);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sums[slice][lane * 4 + i] = s[i];
+  __syncthreads();
+  const int mine = first + threadIdx.x;
+  if (threadIdx.x < kSmallCols && mine < a.d) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlices; ++i) v += sums[i][threadIdx.x];
+    a.dweight[mine] = v;
+  }
+}
+
 // Backward: one chunk per lane up to four wavefronts, whose dots then share
 // a barrier for two rows.
 template <int V, typename F>
@@ -207,8 +290,51 @@ int grad_grid(int64_t T, const RowPlan& p) {
 // the inputs fit the 256 MB last-level cache, it takes 22.2 instead of 19.5.
 constexpr int64_t kGradStreamBytes = int64_t(160) << 20;
 
+// Whether a batch goes through the one-launch kernel: 512 x 2048 takes 12.1 us
+// a call instead of 17.1, 512 x 8192 (16 MB of dy and z) 12.1 instead of 17.2.
+// The 32 slices of a dw column make it slow for many rows: 2048 x 2048 would
+// take 21.7 us instead of 17.0, 8000 x 100 64 instead of 19.
+constexpr int64_t kSmallRows = 1024, kSmallBytes = int64_t(16) << 20;
+constexpr int kSmallPieces = 16;
+
+template <typename X, typename S>
+bool is_small(int64_t T, int d) {
+  return T <= kSmallRows && T * d * int64_t(sizeof(X) + sizeof(S)) <= kSmallBytes &&
+         pieces_of(d, kCols<X, S>) <= kSmallPieces;
+}
+
+bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + nq && b < a + np;
+}
+
+template <typename X, typename S, int C>
+void launch_small(const NormGradArgs& args, hipStream_t st) {
+  NormGradArgs a = args;
+  const int columns = a.dweight ? (a.d + kSmallCols - 1) / kSmallCols : 0;
+  auto launch = [&](int rows, int columns) {
+    a.rows = rows;
+    if (a.d % kCols<X, S> != 0)
+      rms_norm_backward_small_kernel<X, S, true, C>
+          <<<rows + columns, kSmallThreads, 0, st>>>(a);
+    else
+      rms_norm_backward_small_kernel<X, S, false, C>
+          <<<rows + columns, kSmallThreads, 0, st>>>(a);
+  };
+  // Where dz or dx takes the place of dy or z, dw has to read them first.
+  const int64_t nx = a.T * a.d * sizeof(X), ns = a.T * a.d * sizeof(S);
+  if (columns > 0 && (overlap(a.dz, ns, a.dy, nx) || overlap(a.dz, ns, a.z, ns) ||
+                      overlap(a.dx, nx, a.dy, nx) || overlap(a.dx, nx, a.z, ns))) {
+    launch(0, columns);
+    launch(static_cast<int>(a.T), 0);
+  } else {
+    launch(static_cast<int>(a.T), columns);
+  }
+}
+
 template <typename X, typename S>
 size_t partials(int64_t T, int d) {
+  if (is_small<X, S>(T, d)) return 0;
   size_t rows = 0;
   with_backward_plan<kCols<X, S>>(pieces_of(d, kCols<X, S>), [&](auto plan) {
     const RowPlan p = {decltype(plan)::kWaves, decltype(plan)::kChunks};
@@ -219,6 +345,16 @@ size_t partials(int64_t T, int d) {
 
 template <typename X, typename S>
 hipError_t run_bwd(const NormGradArgs& a, hipStream_t st) {
+  if (is_small<X, S>(a.T, a.d)) {
+    const int pieces = pieces_of(a.d, kCols<X, S>);
+    if (pieces <= 4)
+      launch_small<X, S, 1>(a, st);
+    else if (pieces <= 8)
+      launch_small<X, S, 2>(a, st);
+    else
+      launch_small<X, S, 4>(a, st);
+    return hipGetLastError();
+  }
   with_backward_plan<kCols<X, S>>(pieces_of(a.d, kCols<X, S>), [&](auto plan) {
     using P = decltype(plan);
     constexpr int R = grad_rows(P::kChunks);
@@ -251,7 +387,7 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st) {
                                                  : run_bwd<float, float>(a, st);
     if (e != hipSuccess) return e;
   }
-  if (!a.dweight) return hipSuccess;
+  if (!a.dweight || (a.T > 0 && !a.partial)) return hipSuccess;
   const int count = static_cast<int>(rms_norm_backward_partials(a.T, a.d, a.bf16, a.stream_bf16));
   rms_norm_dweight_kernel<<<(a.d + kSumCols - 1) / kSumCols, kSumCols * kSumSlices, 0, st>>>(
       a.partial, count, a.d, a.dweight);

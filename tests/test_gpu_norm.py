@@ -176,7 +176,8 @@ def test_in_place_at_ragged_ends(d, ty):
 @pytest.mark.parametrize("ty,st", PAIRS)
 @pytest.mark.parametrize("T,d", [(1, 1), (1, 2048), (3, 70), (50, 512), (17, 513), (1030, 100),
                                  (700, 767), (1500, 2048), (40, 3001), (5, 8192), (3, 8200),
-                                 (2, 32768)])
+                                 (2, 32768), (22000, 100), (5000, 511), (6000, 513), (5001, 767),
+                                 (1500, 3001), (600, 8192), (300, 8200), (300, 16400), (70, 32768)])
 def test_backward(T, d, ty, st):
     """dz within 64 roundings of its terms' sizes (the dot's chains are the
     sum of squares' above); dw is added over at most ceil(T / 1024) rows (a
@@ -218,8 +219,23 @@ def test_backward_against_differences_of_the_forward():
         assert abs((f(z, w + h * ew) - f(z, w - h * ew)) / (2 * h) - (f64(g.dweight) * f64(ew)).sum()) < 1e-4 * size
 
 
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d", [(40, 770), (3, 2048), (5000, 770)])
+def test_backward_over_its_inputs(T, d, ty):
+    """dz in the place of dy, z or the residual's gradient, small and large:
+    the same bits, dweight (which reads dy and z) too."""
+    rng = np.random.default_rng(T)
+    z, w, dy, dres = (randn(rng, s, ty) for s in ((T, d), (d,), (T, d), (T, d)))
+    rstd = fff.rms_norm(z, w, want_rstd=True).rstd
+    want = fff.rms_norm_backward(dy, z, w, rstd, dresidual=dres)
+    for k in range(3):
+        t = [dy.clone(), z.clone(), dres.clone()]
+        g = fff.rms_norm_backward(t[0], t[1], w, rstd, dresidual=t[2], dz=t[k])
+        assert torch.equal(t[k], want.dz) and torch.equal(g.dweight, want.dweight)
+
+
 def test_backward_in_place_without_dweight_and_same_every_time():
-    T, d = 3000, 770
+    T, d = 6000, 770
     rng = np.random.default_rng(6)
     z, w, dy, dres = (randn(rng, s, "bf16") for s in ((T, d), (d,), (T, d), (T, d)))
     rstd = fff.rms_norm(z, w, want_rstd=True).rstd

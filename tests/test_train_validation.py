@@ -79,7 +79,7 @@ def test_no_rows_touches_nothing(lib):
 
 
 def test_norm_backward_pointers_and_workspace(lib):
-    s = norm_shape(T=300)
+    s = norm_shape(T=30000)
     need = ctypes.c_size_t()
     assert lib.fff_rms_norm_backward_workspace_size(s, ctypes.byref(need)) == fff.SUCCESS
     assert need.value >= 64 * 4 and lib.fff_rms_norm_backward_workspace_size(s, None) == fff.ERROR_INVALID_VALUE
