@@ -5,7 +5,7 @@
 //
 // Rows are held as in the forward pass; a team takes every so many-th row and
 // keeps its columns' share of dw in registers, so that dw costs one partial
-// sum of d columns per team and a second kernel that adds them in a fixed
+// sum of d columns per workgroup and a second kernel that adds them in a fixed
 // order (no atomics: the same bits on every call).
 //
 // Bound by HBM: T = 16384, d = 2048 in bf16 with the residual's gradient moves
@@ -20,7 +20,7 @@ namespace {
 
 // R rows at a time per team, whose dots share a barrier; the columns' share
 // of dw stays in registers over the team's rows and goes to the workspace
-// once per team.
+// once per workgroup.
 template <typename X, typename S, bool RAGGED, int WAVES, int C, int R, bool STREAM>
 __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_backward_kernel(NormGradArgs a) {
   constexpr int V = kCols<X, S>;
@@ -125,11 +125,25 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_backward_kernel
     }
   }
   if (!a.partial) return;
-  float* out = a.partial + (size_t(blockIdx.x) * kRows + threadIdx.x / kTeam) * a.d;
+  if constexpr (kRows > 1) {  // the workgroup's teams as one partial sum
+    __shared__ float sums[kRows][C * V][kTeam];
+    const int team = threadIdx.x / kTeam;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    At((c * kTeam + lane) * V, a.d).store_floats(acc[c], out);
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sums[team][c * V + i][lane] = acc[c][i];
+    __syncthreads();
+    if (team != 0) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 1; k < kRows; ++k) acc[c][i] += sums[k][c * V + i][lane];
   }
+  float* out = a.partial + size_t(blockIdx.x) * a.d;
+#pragma unroll
+  for (int c = 0; c < C; ++c) At((c * kTeam + lane) * V, a.d).store_floats(acc[c], out);
 }
 
 // dw[j] = sum over the partials in a fixed order: 32 columns (a 128-byte line
@@ -338,7 +352,7 @@ size_t partials(int64_t T, int d) {
   size_t rows = 0;
   with_backward_plan<kCols<X, S>>(pieces_of(d, kCols<X, S>), [&](auto plan) {
     const RowPlan p = {decltype(plan)::kWaves, decltype(plan)::kChunks};
-    rows = T == 0 ? 0 : size_t(grad_grid(T, p)) * p.rows();
+    rows = T == 0 ? 0 : grad_grid(T, p);
   });
   return rows;
 }
