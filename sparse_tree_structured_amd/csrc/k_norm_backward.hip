@@ -391,7 +391,9 @@ hipError_t run_bwd(const NormGradArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t rms_norm_backward_partials(int64_t T, int d, bool bf16, bool stream_bf16) {
-  return bf16 && stream_bf16 ? partials<uint16_t, uint16_t>(T, d) : partials<float, float>(T, d);
+  return bf16 && stream_bf16 ? partials<uint16_t, uint16_t>(T, d)
+         : bf16              ? partials<uint16_t, float>(T, d)
+                             : partials<float, float>(T, d);
 }
 
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st) {
@@ -401,8 +403,8 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st) {
                                                  : run_bwd<float, float>(a, st);
     if (e != hipSuccess) return e;
   }
-  if (!a.dweight || (a.T > 0 && !a.partial)) return hipSuccess;
   const int count = static_cast<int>(rms_norm_backward_partials(a.T, a.d, a.bf16, a.stream_bf16));
+  if (!a.dweight || (a.T > 0 && count == 0)) return hipSuccess;  // a small batch has written dw
   rms_norm_dweight_kernel<<<(a.d + kSumCols - 1) / kSumCols, kSumCols * kSumSlices, 0, st>>>(
       a.partial, count, a.d, a.dweight);
   return hipGetLastError();
