@@ -784,7 +784,8 @@ class TensorTable:
     """The tensors of an optimiser, laid out for the library: made once by
     adamw_table or grad_table, used at every step.  It keeps the tensors
     alive; they are updated in place and must keep their storage (make
-    another table where a tensor is replaced)."""
+    another table where a tensor is replaced).  One stream uses it at a time,
+    as for the tensors themselves."""
 
     def __init__(self, entries, first, state_code, keep):
         self.entries = entries        # array of AdamwTensor
@@ -798,6 +799,7 @@ class TensorTable:
         if st != SUCCESS:
             raise FFFError(st, "fff_grad_norm_workspace_size")
         self.norm_workspace = n.value
+        self._workspace = (None, None)  # the stream it belongs to, and grad_norm's workspace
 
 
 def _flat(t, n, dtypes, device, what):
@@ -939,7 +941,10 @@ def grad_norm(grads, *, max_norm: float = float("inf"), out=None, workspace=None
         pws = _tensor(workspace, (have,), torch.uint8, dev, "workspace")
     elif table.norm_workspace:
         have = table.norm_workspace
-        workspace = _empty((have,), torch.uint8, dev, stream)
+        kept, workspace = table._workspace
+        if kept != handle:  # memory of this stream, so that its reuse is in order
+            workspace = _empty((have,), torch.uint8, dev, stream)
+            table._workspace = (handle, workspace)
         pws = workspace.data_ptr()
     st = load_library().fff_grad_norm(table.entries, table.count, max_norm, pout, pws, have, handle)
     if st != SUCCESS:

@@ -131,6 +131,7 @@ void with_forward_plan(int pieces, const F& f) {
   else if (pieces <= 4) f(Plan<2, 2>());
   else if (pieces <= 8) f(Plan<4, 2>());
   else if (pieces <= 16) f(Plan<8, 2>());
+  else if (pieces <= 24) f(Plan<8, 3>());
   else if (pieces <= 32) f(Plan<8, 4>());
   else if (V == 8 || pieces <= 64) f(Plan<16, 4>());
   else if constexpr (V == 4) f(Plan<16, 8>());

@@ -182,17 +182,17 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void rms_norm_dweight_kernel
 // Small batches in one launch, without a workspace: the first a.rows (T, or
 // none) workgroups have a row of dz each, and the others 32 columns of dw, for
 // which they read dy and z once more (dw needs no row's dot).
-constexpr int kSmallThreads = 256, kSmallCols = 32;
+constexpr int kSmallCols = 32;
 
-template <typename X, typename S, bool RAGGED, int C>
-__global__ __launch_bounds__(kSmallThreads) void rms_norm_backward_small_kernel(NormGradArgs a) {
+template <typename X, typename S, bool RAGGED, int THREADS, int C>
+__global__ __launch_bounds__(THREADS) void rms_norm_backward_small_kernel(NormGradArgs a) {
   constexpr int V = kCols<X, S>;
   const X* dy = static_cast<const X*>(a.dy);
   const S* zin = static_cast<const S*>(a.z);
   const float inv_d = 1.0f / static_cast<float>(a.d);
   if (static_cast<int>(blockIdx.x) < a.rows) {
     using At = Span<V, RAGGED>;
-    __shared__ float lds[kSmallThreads / kWave];
+    __shared__ float lds[THREADS / kWave];
     const X* w = static_cast<const X*>(a.weight);
     const S* dres = static_cast<const S*>(a.dresidual);
     S* dz = static_cast<S*>(a.dz);
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(kSmallThreads) void rms_norm_backward_small_kernel(
     Pack<S, V> zr[C], er[C] = {};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const At at((c * kSmallThreads + threadIdx.x) * V, a.d);
+      const At at((c * THREADS + threadIdx.x) * V, a.d);
       at.template load<false>(yr[c], dy + row);
       at.template load<false>(zr[c], zin + row);
       if (w) at.template load<false>(wr[c], w);
@@ -216,14 +216,14 @@ __global__ __launch_bounds__(kSmallThreads) void rms_norm_backward_small_kernel(
       float g[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) g[i] = yr[c].get(i) * (wr[c].get(i) + offset);
-      At((c * kSmallThreads + threadIdx.x) * V, a.d).clear(g);
+      At((c * THREADS + threadIdx.x) * V, a.d).clear(g);
 #pragma unroll
       for (int i = 0; i < V; ++i) dot += g[i] * (zr[c].get(i) * rstd);
     }
-    dot = team_total<kSmallThreads / kWave>(dot, lds) * inv_d;
+    dot = team_total<THREADS / kWave>(dot, lds) * inv_d;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const At at((c * kSmallThreads + threadIdx.x) * V, a.d);
+      const At at((c * THREADS + threadIdx.x) * V, a.d);
       float v[V];
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -233,8 +233,8 @@ __global__ __launch_bounds__(kSmallThreads) void rms_norm_backward_small_kernel(
     }
     return;
   }
-  // 32 slices of the rows by eight lanes of four columns.
-  constexpr int kLanes = kSmallCols / 4, kSlices = kSmallThreads / kLanes;
+  // Slices of the rows by eight lanes of four columns.
+  constexpr int kLanes = kSmallCols / 4, kSlices = THREADS / kLanes;
   __shared__ float sums[kSlices][kSmallCols + 1];
   const int lane = threadIdx.x % kLanes, slice = threadIdx.x / kLanes;
   const int first = (static_cast<int>(blockIdx.x) - a.rows) * kSmallCols;
@@ -272,7 +272,9 @@ void with_backward_plan(int pieces, const F& f) {
   else if (pieces <= 4) f(Plan<4, 1>());
   else if (pieces <= 6) f(Plan<3, 2>());
   else if (pieces <= 8) f(Plan<4, 2>());
+  else if (pieces <= 12) f(Plan<4, 3>());
   else if (pieces <= 16) f(Plan<4, 4>());
+  else if (pieces <= 24) f(Plan<8, 3>());
   else if (pieces <= 32) f(Plan<8, 4>());
   else if (V == 8 || pieces <= 64) f(Plan<16, 4>());
   else if constexpr (V == 4) f(Plan<16, 8>());
@@ -306,10 +308,10 @@ constexpr int64_t kGradStreamBytes = int64_t(160) << 20;
 
 // Whether a batch goes through the one-launch kernel: 512 x 2048 takes 12.1 us
 // a call instead of 17.1, 512 x 8192 (16 MB of dy and z) 12.1 instead of 17.2.
-// The 32 slices of a dw column make it slow for many rows: 2048 x 2048 would
+// The few slices of a dw column make it slow for many rows: 2048 x 2048 would
 // take 21.7 us instead of 17.0, 8000 x 100 64 instead of 19.
 constexpr int64_t kSmallRows = 1024, kSmallBytes = int64_t(16) << 20;
-constexpr int kSmallPieces = 16;
+constexpr int kSmallPieces = 32;
 
 template <typename X, typename S>
 bool is_small(int64_t T, int d) {
@@ -322,18 +324,18 @@ bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
   return p && q && a < b + nq && b < a + np;
 }
 
-template <typename X, typename S, int C>
+template <typename X, typename S, int THREADS, int C>
 void launch_small(const NormGradArgs& args, hipStream_t st) {
   NormGradArgs a = args;
   const int columns = a.dweight ? (a.d + kSmallCols - 1) / kSmallCols : 0;
   auto launch = [&](int rows, int columns) {
     a.rows = rows;
     if (a.d % kCols<X, S> != 0)
-      rms_norm_backward_small_kernel<X, S, true, C>
-          <<<rows + columns, kSmallThreads, 0, st>>>(a);
+      rms_norm_backward_small_kernel<X, S, true, THREADS, C>
+          <<<rows + columns, THREADS, 0, st>>>(a);
     else
-      rms_norm_backward_small_kernel<X, S, false, C>
-          <<<rows + columns, kSmallThreads, 0, st>>>(a);
+      rms_norm_backward_small_kernel<X, S, false, THREADS, C>
+          <<<rows + columns, THREADS, 0, st>>>(a);
   };
   // Where dz or dx takes the place of dy or z, dw has to read them first.
   const int64_t nx = a.T * a.d * sizeof(X), ns = a.T * a.d * sizeof(S);
@@ -362,11 +364,13 @@ hipError_t run_bwd(const NormGradArgs& a, hipStream_t st) {
   if (is_small<X, S>(a.T, a.d)) {
     const int pieces = pieces_of(a.d, kCols<X, S>);
     if (pieces <= 4)
-      launch_small<X, S, 1>(a, st);
+      launch_small<X, S, 256, 1>(a, st);
     else if (pieces <= 8)
-      launch_small<X, S, 2>(a, st);
+      launch_small<X, S, 256, 2>(a, st);
+    else if (pieces <= 16)
+      launch_small<X, S, 256, 4>(a, st);
     else
-      launch_small<X, S, 4>(a, st);
+      launch_small<X, S, 512, 4>(a, st);
     return hipGetLastError();
   }
   with_backward_plan<kCols<X, S>>(pieces_of(a.d, kCols<X, S>), [&](auto plan) {

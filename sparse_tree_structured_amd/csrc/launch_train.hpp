@@ -92,7 +92,7 @@ hipError_t launch_adamw(const AdamwArgs& a, int blocks, int param, bool grad_bf1
                         bool stochastic, hipStream_t st);
 
 constexpr int kNormChunk = 16384;     // gradient elements per workgroup
-constexpr int kNormSmallChunk = 1024;  // per wavefront, for a small list
+constexpr int kNormSmallChunk = 2048;  // per wavefront, for a small list
 constexpr int kNormSmallChunks = 64;   // of at most so many of these
 constexpr int kNormMaxTensors = 192;
 

@@ -298,7 +298,8 @@ def test_elements_past_32_bits():
 
 
 @pytest.mark.parametrize("sizes", [[1], [5, 16384, 16385, 3], [0, 700], [100003], [50] * 350, [0],
-                                   [65536], [65537], [1024] * 64, [1025] * 32, [1] * 65, [60000, 0, 7]])
+                                   [65536], [65537], [1024] * 64, [1025] * 32, [1] * 65, [60000, 0, 7],
+                                   [131072], [131073], [2048] * 64, [2049] * 33])
 @pytest.mark.parametrize("grad", ["f32", "bf16"])
 def test_grad_norm(sizes, grad):
     """Squares are summed in 64 bits: the result is off by its rounding to 32
