@@ -335,6 +335,9 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) 
   if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
 }
 
+// The sum of the partials, in one order.  A second launch: with a count of
+// the workgroups that are done, by which the last one would do this itself,
+// 1054 atomics on one address made 24 us of 14.
 __global__ __launch_bounds__(1024) void grad_norm_final_kernel(const double* partial, int64_t count,
                                                                double max_norm, float* out) {
   double s = 0.0;

@@ -146,7 +146,7 @@ def test_adamw_nothing_to_do(lib):
 
 
 def test_grad_norm(lib):
-    t = (fff.AdamwTensor * 1)(entry(n=100000))
+    t = (fff.AdamwTensor * 1)(entry(n=1000000))
     n = ctypes.c_size_t()
     assert lib.fff_grad_norm_workspace_size(t, 1, ctypes.byref(n)) == fff.SUCCESS and n.value >= 8
     assert lib.fff_grad_norm_workspace_size(t, 1, None) == fff.ERROR_INVALID_VALUE
