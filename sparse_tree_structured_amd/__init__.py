@@ -610,40 +610,68 @@ class RmsNormGrad(NamedTuple):
 _norm_shape = functools.lru_cache(maxsize=256)(NormShape)
 
 
-def _here(t, stream):
+class _Torch:
+    """What a call needs of torch, looked up once: small calls are bound by
+    the host."""
+
+    def __init__(self):
+        import torch
+        self.f32, self.bf16, self.f8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+        self.u8 = torch.uint8
+        self.codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+        self.empty, self.stream = torch.empty, torch.cuda.stream
+        self.device = getattr(torch._C, "_cuda_getDevice", None)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+_lazy: Optional[_Torch] = None
+
+
+def _rt() -> _Torch:
+    global _lazy
+    if _lazy is None:
+        _lazy = _Torch()
+    return _lazy
+
+
+def _here(rt, t, stream):
     """The handle of the stream to launch on: `stream`, or the current one.
     The library launches on the current device, so tensors must be there."""
-    torch = _torch()
     index = t.get_device()
     if index < 0:
         raise ValueError(f"tensors must be on a GPU, not {t.device}")
-    if index != torch._C._cuda_getDevice():
+    if index != rt.device():
         raise ValueError(f"tensors are on {t.device}, which is not the current device")
-    if stream is not None:
-        return int(stream.cuda_stream)
-    return torch._C._cuda_getCurrentRawStream(index)
+    return rt.raw_stream(index) if stream is None else int(stream.cuda_stream)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(rt, shape, dtype, device, stream):
     """A new tensor that belongs to the stream it is used on."""
-    torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return rt.empty(shape, dtype=dtype, device=device)
+    with rt.stream(stream):
+        return rt.empty(shape, dtype=dtype, device=device)
 
 
-def _tensor(t, shape, dtype, device, what):
-    """The pointer of a tensor that must have this shape, dtype and device
-    and be contiguous."""
-    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+def _code(rt, dtype) -> int:
+    code = rt.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _tensor(t, shape, dtype, like, what):
+    """The pointer of a tensor that must have this shape and dtype, be
+    contiguous, and lie on the device of `like`."""
+    if (t.shape == shape and t.dtype is dtype and t.is_contiguous()
+            and t.get_device() == like.get_device()):
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if t.device != like.device:
+        raise ValueError(f"{what} must be on {like.device}, got {t.device}")
     raise ValueError(f"{what} must be contiguous")
 
 
@@ -658,58 +686,57 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
     there is no residual.  ``out_dtype`` torch.float8_e4m3fn (or a ``y`` of
     that dtype) gives y in 8 bits with a scale per row, or per ``group`` = 32,
     64 or 128 columns.  ``residual_out`` may be ``residual`` itself."""
-    torch = _torch()
-    shape, dev = x.shape, x.device
+    rt = _rt()
+    shape, ty = x.shape, x.dtype
     if len(shape) != 2:
         raise ValueError(f"x [T,d] must have 2 dimensions, got shape {tuple(shape)}")
     T, d = shape
-    xty = x.dtype
-    px, pr, pw, pz, prs, ps = _tensor(x, shape, xty, dev, "x"), 0, 0, 0, 0, 0
-    ty = xty if weight is None else weight.dtype
+    stream_ty = ty if residual is None else residual.dtype
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    px, pr, pw, pz, prs, ps = x.data_ptr(), 0, 0, 0, 0, 0
     if weight is not None:
-        pw = _tensor(weight, (d,), ty, dev, "weight [d]")
-    if residual is None:
-        stream_ty = xty
-    else:
-        stream_ty = residual.dtype
-        pr = _tensor(residual, shape, stream_ty, dev, "residual")
-        if xty is not ty:
-            raise ValueError(f"x must be {ty} beside a residual, got {xty}")
-    code, stream_code = _type_code(ty, torch), _type_code(stream_ty, torch)
+        ty = weight.dtype
+        pw = _tensor(weight, (d,), ty, x, "weight [d]")
+    if residual is not None:
+        pr = _tensor(residual, shape, stream_ty, x, "residual")
+        if x.dtype is not ty:
+            raise ValueError(f"x must be {ty} beside a residual, got {x.dtype}")
+    code, stream_code = _code(rt, ty), _code(rt, stream_ty)
     out_ty = y.dtype if y is not None else (out_dtype or ty)
     if out_dtype is not None and out_ty is not out_dtype:
         raise ValueError(f"y must be {out_dtype}, got {out_ty}")
-    e4m3 = out_ty is torch.float8_e4m3fn
+    e4m3 = out_ty is rt.f8
     if not e4m3 and out_ty is not ty:
-        raise ValueError(f"y must be {ty} or torch.float8_e4m3fn, got {out_ty}")
-    handle = _here(x, stream)
+        raise ValueError(f"y must be {ty} or {rt.f8}, got {out_ty}")
+    handle = _here(rt, x, stream)
     if residual is None and stream_ty is not ty:  # x is the stream itself
         px, pr = 0, px
-    if y is None:
-        y = _empty(shape, out_ty, dev, stream)
-        py = y.data_ptr()
+    if y is not None:
+        py = _tensor(y, shape, out_ty, x, "y")
     else:
-        py = _tensor(y, shape, out_ty, dev, "y")
+        y = _empty(rt, shape, out_ty, x.device, stream)
+        py = y.data_ptr()
     if residual_out is not None:
-        pz = _tensor(residual_out, shape, stream_ty, dev, "residual_out")
+        pz = _tensor(residual_out, shape, stream_ty, x, "residual_out")
     elif residual is not None:
-        residual_out = _empty(shape, stream_ty, dev, stream)
+        residual_out = _empty(rt, shape, stream_ty, x.device, stream)
         pz = residual_out.data_ptr()
     if rstd is not None:
-        prs = _tensor(rstd, (T,), torch.float32, dev, "rstd [T]")
+        prs = _tensor(rstd, (T,), rt.f32, x, "rstd [T]")
     elif want_rstd:
-        rstd = _empty((T,), torch.float32, dev, stream)
+        rstd = _empty(rt, (T,), rt.f32, x.device, stream)
         prs = rstd.data_ptr()
     if e4m3:
         groups = (T, -(-d // group) if group > 0 else 1)
-        if scale is None:
-            scale = _empty(groups, torch.float32, dev, stream)
-            ps = scale.data_ptr()
+        if scale is not None:
+            ps = _tensor(scale, groups, rt.f32, x, "scale [T, groups]")
         else:
-            ps = _tensor(scale, groups, torch.float32, dev, "scale [T, groups]")
+            scale = _empty(rt, groups, rt.f32, x.device, stream)
+            ps = scale.data_ptr()
     elif scale is not None:
-        raise ValueError("scale is for a y of torch.float8_e4m3fn")
-    st = load_library().fff_rms_norm(
+        raise ValueError(f"scale is for a y of {rt.f8}")
+    st = (_lib or load_library()).fff_rms_norm(
         _norm_shape(T, d, code, stream_code, DTYPE_E4M3 if e4m3 else code, group, eps, weight_offset),
         px, pr, pw, py, ps, pz, prs, handle)
     if st != SUCCESS:
@@ -735,44 +762,45 @@ def rms_norm_backward(dy, z, weight, rstd, *, dresidual=None, weight_offset: flo
     what it normalised (its residual_out, or x), ``rstd`` its rstd and
     ``dresidual`` the gradient that reaches residual_out.  Where z is float32
     beside a bf16 layer, dx is dz once more in bf16."""
-    torch = _torch()
-    shape, dev = dy.shape, dy.device
+    rt = _rt()
+    shape, ty, zty, f32 = dy.shape, dy.dtype, z.dtype, rt.f32
     if len(shape) != 2:
         raise ValueError(f"dy [T,d] must have 2 dimensions, got shape {tuple(shape)}")
     T, d = shape
-    ty, zty, f32 = dy.dtype, z.dtype, torch.float32
-    pdy = _tensor(dy, shape, ty, dev, "dy")
-    pz = _tensor(z, shape, zty, dev, "z")
-    pw = _tensor(weight, (d,), ty, dev, "weight [d]") if weight is not None else 0
-    pr = _tensor(rstd, (T,), f32, dev, "rstd [T]")
-    pe = _tensor(dresidual, shape, zty, dev, "dresidual") if dresidual is not None else 0
-    code, zcode = _type_code(ty, torch), _type_code(zty, torch)
-    handle = _here(dy, stream)
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    pdy = dy.data_ptr()
+    pz = _tensor(z, shape, zty, dy, "z")
+    pw = _tensor(weight, (d,), ty, dy, "weight [d]") if weight is not None else 0
+    pr = _tensor(rstd, (T,), f32, dy, "rstd [T]")
+    pe = _tensor(dresidual, shape, zty, dy, "dresidual") if dresidual is not None else 0
+    code, zcode = _code(rt, ty), _code(rt, zty)
+    handle = _here(rt, dy, stream)
     pdx = pdw = pws = have = 0
-    if dz is None:
-        dz = _empty(shape, zty, dev, stream)
-        pdz = dz.data_ptr()
+    if dz is not None:
+        pdz = _tensor(dz, shape, zty, dy, "dz")
     else:
-        pdz = _tensor(dz, shape, zty, dev, "dz")
+        dz = _empty(rt, shape, zty, dy.device, stream)
+        pdz = dz.data_ptr()
     if dx is not None:
-        pdx = _tensor(dx, shape, ty, dev, "dx")
+        pdx = _tensor(dx, shape, ty, dy, "dx")
     elif zty is not ty:
-        dx = _empty(shape, ty, dev, stream)
+        dx = _empty(rt, shape, ty, dy.device, stream)
         pdx = dx.data_ptr()
     if dweight is not None:
-        pdw = _tensor(dweight, (d,), f32, dev, "dweight [d]")
+        pdw = _tensor(dweight, (d,), f32, dy, "dweight [d]")
     elif want_dweight:
-        dweight = _empty((d,), f32, dev, stream)
+        dweight = _empty(rt, (d,), f32, dy.device, stream)
         pdw = dweight.data_ptr()
     if workspace is not None:
         have = workspace.numel()
-        pws = _tensor(workspace, (have,), torch.uint8, dev, "workspace")
+        pws = _tensor(workspace, (have,), rt.u8, dy, "workspace")
     elif dweight is not None:
         have = rms_norm_backward_workspace_size(T, d, code, zcode)
         if have:
-            workspace = _empty((have,), torch.uint8, dev, stream)
+            workspace = _empty(rt, (have,), rt.u8, dy.device, stream)
             pws = workspace.data_ptr()
-    st = load_library().fff_rms_norm_backward(
+    st = (_lib or load_library()).fff_rms_norm_backward(
         _norm_shape(T, d, code, zcode, code, 0, 0.0, weight_offset), pdy, pz, pw, pr, pe, pdz, pdx,
         pdw, pws, have, handle)
     if st != SUCCESS:
@@ -907,16 +935,16 @@ def adamw_step(table: TensorTable, *, lr: float, step: int, beta1: float = 0.9,
     step changes nothing.  ``seed``: None rounds to nearest, a number (another
     one at every step) rounds 8-bit states and bf16 params without a master
     stochastically."""
-    torch = _torch()
+    rt = _rt()
     if table.state_code is None:
         raise ValueError("the table holds gradients only: make it with adamw_table")
     ps = 0
     if grad_scale is not None:
-        ps = _flat(grad_scale, 1, (torch.float32,), table.device, "grad_scale")
-    handle = _here(table.first, stream)
+        ps = _flat(grad_scale, 1, (rt.f32,), table.device, "grad_scale")
+    handle = _here(rt, table.first, stream)
     config = AdamwConfig(lr, beta1, beta2, eps, step, table.state_code, seed is not None,
                          0 if seed is None else seed & 0xFFFFFFFFFFFFFFFF, ps)
-    st = load_library().fff_adamw_step(config, table.entries, table.count, handle)
+    st = (_lib or load_library()).fff_adamw_step(config, table.entries, table.count, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_adamw_step")
 
@@ -926,27 +954,26 @@ def grad_norm(grads, *, max_norm: float = float("inf"), out=None, workspace=None
     tensor [2], the norm of all gradients together and the factor
     min(1, max_norm / (norm + 1e-6)) (NaN where the norm is not finite) that
     adamw_step takes as ``grad_scale`` (``out[1:]``)."""
-    torch = _torch()
+    rt = _rt()
     table = grads if isinstance(grads, TensorTable) else grad_table(grads)
-    dev = table.device
-    handle = _here(table.first, stream)
+    handle = _here(rt, table.first, stream)
     pws = have = 0
     if out is None:
-        out = _empty((2,), torch.float32, dev, stream)
+        out = _empty(rt, (2,), rt.f32, table.device, stream)
         pout = out.data_ptr()
     else:
-        pout = _tensor(out, (2,), torch.float32, dev, "out [2]")
+        pout = _tensor(out, (2,), rt.f32, table.first, "out [2]")
     if workspace is not None:
         have = workspace.numel()
-        pws = _tensor(workspace, (have,), torch.uint8, dev, "workspace")
+        pws = _tensor(workspace, (have,), rt.u8, table.first, "workspace")
     elif table.norm_workspace:
         have = table.norm_workspace
         kept, workspace = table._workspace
         if kept != handle:  # memory of this stream, so that its reuse is in order
-            workspace = _empty((have,), torch.uint8, dev, stream)
+            workspace = _empty(rt, (have,), rt.u8, table.device, stream)
             table._workspace = (handle, workspace)
         pws = workspace.data_ptr()
-    st = load_library().fff_grad_norm(table.entries, table.count, max_norm, pout, pws, have, handle)
+    st = (_lib or load_library()).fff_grad_norm(table.entries, table.count, max_norm, pout, pws, have, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_grad_norm")
     return out
