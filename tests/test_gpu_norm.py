@@ -275,14 +275,15 @@ def test_forward_of_large_batches_past_the_caches(mb, ty, st, d, out):
         assert out is None or torch.equal(o.scale[a:a + n], part.scale)
 
 
-@pytest.mark.parametrize("ty,st,d", [("bf16", "bf16", 4099), ("bf16", "bf16", 4096), ("f32", "f32", 2051)])
+@pytest.mark.parametrize("ty,st,d", [("bf16", "bf16", 4099), ("bf16", "bf16", 4096), ("f32", "f32", 2051),
+                                     ("bf16", "f32", 2050), ("bf16", "f32", 2048)])
 def test_backward_of_large_batches_past_the_caches(ty, st, d):
     """A batch large enough for streaming reads against its rows a part at a
     time (which are not), and dweight against the parts' sum."""
     T = (180 << 20) // (d * 3 * (2 if ty == "bf16" else 4))
     gen = torch.Generator(device=DEV)
     gen.manual_seed(d)
-    dy, z, dres = (torch.randn(T, d, generator=gen, device=DEV).to(TY[ty]) for _ in range(3))
+    dy, z, dres = (torch.randn(T, d, generator=gen, device=DEV).to(TY[k]) for k in (ty, st, st))
     w = torch.randn(d, generator=gen, device=DEV).to(TY[ty])
     rstd = fff.rms_norm(z, w, want_rstd=True).rstd
     print(f"[gpu] rms_norm_backward large T={T} d={d} {ty}", flush=True)
@@ -290,7 +291,7 @@ def test_backward_of_large_batches_past_the_caches(ty, st, d):
     dw, n = torch.zeros(d, dtype=torch.float64, device=DEV), T // 4 + 1
     for a in range(0, T, n):
         part = fff.rms_norm_backward(dy[a:a + n], z[a:a + n], w, rstd[a:a + n], dresidual=dres[a:a + n])
-        assert torch.equal(g.dz[a:a + n], part.dz)
+        assert torch.equal(g.dz[a:a + n], part.dz) and torch.equal(g.dx[a:a + n], part.dx)
         dw += part.dweight.double()
     size = (dy.float().abs() * z.float().abs() * rstd[:, None]).sum(0).double()
     assert bool(((g.dweight.double() - dw).abs() <= size * 2 * (64 + T / 512 + 256) * O.U32).all())
