@@ -827,7 +827,9 @@ class TensorTable:
         if st != SUCCESS:
             raise FFFError(st, "fff_grad_norm_workspace_size")
         self.norm_workspace = n.value
-        self._workspace = (None, None)  # the stream it belongs to, and grad_norm's workspace
+        # grad_norm's workspace on every stream that has used the table: kept as
+        # long as the table, for a captured graph keeps its address.
+        self._workspaces = {}
 
 
 def _flat(t, n, dtypes, device, what):
@@ -968,10 +970,9 @@ def grad_norm(grads, *, max_norm: float = float("inf"), out=None, workspace=None
         pws = _tensor(workspace, (have,), rt.u8, table.first, "workspace")
     elif table.norm_workspace:
         have = table.norm_workspace
-        kept, workspace = table._workspace
-        if kept != handle:  # memory of this stream, so that its reuse is in order
-            workspace = _empty(rt, (have,), rt.u8, table.device, stream)
-            table._workspace = (handle, workspace)
+        workspace = table._workspaces.get(handle)
+        if workspace is None:
+            workspace = table._workspaces[handle] = _empty(rt, (have,), rt.u8, table.device, stream)
         pws = workspace.data_ptr()
     st = (_lib or load_library()).fff_grad_norm(table.entries, table.count, max_norm, pout, pws, have, handle)
     if st != SUCCESS:

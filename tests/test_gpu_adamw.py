@@ -358,3 +358,25 @@ def test_on_another_stream_and_in_a_graph():
         step(t)
         graph.replay()
         check()
+
+
+def test_a_table_keeps_the_workspace_of_a_captured_norm():
+    """A norm with a workspace, captured, then used eagerly on two streams:
+    every replay gives the eager result and touches nothing else."""
+    g = torch.randn(300_000, device=DEV)
+    table = fff.grad_table([g])
+    side = torch.cuda.Stream()
+    fff.grad_norm(table, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = fff.grad_norm(table)
+    for k in range(4):
+        g.normal_()
+        torch.cuda.synchronize()
+        want = fff.grad_norm(table)
+        other = [torch.full((64,), 7.0, device=DEV) for _ in range(20)]
+        fff.grad_norm(table, stream=side)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and all(bool((o == 7.0).all()) for o in other)
