@@ -51,11 +51,13 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
       if (x) at.template load<STREAM == kStreamAll>(xr[c], x + row);
       if (r) at.template load<STREAM == kStreamAll>(rr[c], r + row);
     }
+    auto load_weight = [&]() {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const At at((c * kTeam + lane) * V, a.d);
-      if (w) at.template load<false>(wr[c], w);
-    }
+      for (int c = 0; c < C; ++c)
+        if (w) At((c * kTeam + lane) * V, a.d).template load<false>(wr[c], w);
+    };
+    // With the row if the registers hold it; eight chunks of one leave no room.
+    if constexpr (C < 8) load_weight();
     float z[C][V];
     float ss = 0.0f;
 #pragma unroll
@@ -70,6 +72,7 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
       if (zout) at.template store<STREAM != kStreamNone>(packed<S, V>(z[c]), zout + row);
     }
     ss = team_total<WAVES>(ss, lds_f);
+    if constexpr (C == 8) load_weight();
     const float rstd = 1.0f / sqrtf(ss * inv_d + a.eps);
     if (a.rstd && lane == 0) a.rstd[t] = rstd;
 #pragma unroll

@@ -182,13 +182,14 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void rms_norm_dweight_kernel
   }
 }
 
-// Small batches in one launch, without a workspace: the first a.rows (T, or
-// none) workgroups have a row of dz each, and the others 32 columns of dw, for
-// which they read dy and z once more (dw needs no row's dot).
+// Small batches, and the widest rows, in one launch without a workspace: the
+// first a.rows (T, or none) workgroups have a row of dz each, and the others 32
+// columns of dw, for which they read dy and z once more (dw needs no row's
+// dot).
 constexpr int kSmallCols = 32;
 
 template <typename X, typename S, bool RAGGED, int THREADS, int C>
-__global__ __launch_bounds__(THREADS) void rms_norm_backward_small_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(THREADS) void rms_norm_backward_rows_columns_kernel(NormGradArgs a) {
   constexpr int V = kCols<X, S>;
   const X* dy = static_cast<const X*>(a.dy);
   const S* zin = static_cast<const S*>(a.z);
@@ -213,15 +214,14 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_small_kernel(NormGr
       if (w) at.template load<false>(wr[c], w);
       if (dres) at.template load<false>(er[c], dres + row);
     }
-    float dot = 0.0f;
+    float g[C][V], dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float g[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = yr[c].get(i) * (wr[c].get(i) + offset);
-      At((c * THREADS + threadIdx.x) * V, a.d).clear(g);
+      for (int i = 0; i < V; ++i) g[c][i] = yr[c].get(i) * (wr[c].get(i) + offset);
+      At((c * THREADS + threadIdx.x) * V, a.d).clear(g[c]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) dot += g[i] * (zr[c].get(i) * rstd);
+      for (int i = 0; i < V; ++i) dot += g[c][i] * (zr[c].get(i) * rstd);
     }
     dot = team_total<THREADS / kWave>(dot, lds) * inv_d;
 #pragma unroll
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_small_kernel(NormGr
       float v[V];
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        v[i] = rstd * (yr[c].get(i) * (wr[c].get(i) + offset) - zr[c].get(i) * rstd * dot) + er[c].get(i);
+        v[i] = rstd * (g[c][i] - zr[c].get(i) * rstd * dot) + er[c].get(i);
       at.store(packed<S, V>(v), dz + row);
       if (dx) at.store(packed<X, V>(v), dx + row);
     }
@@ -278,9 +278,8 @@ void with_backward_plan(int pieces, const F& f) {
   else if (pieces <= 12) f(Plan<4, 3>());
   else if (pieces <= 16) f(Plan<4, 4>());
   else if (pieces <= 24) f(Plan<8, 3>());
-  else if (pieces <= 32) f(Plan<8, 4>());
-  else if (V == 8 || pieces <= 64) f(Plan<16, 4>());
-  else if constexpr (V == 4) f(Plan<16, 8>());
+  else if (V == 8 || pieces <= 32) f(Plan<8, 4>());
+  else if constexpr (V == 4) f(Plan<16, 4>());
 }
 
 // Rows of the backward at a time: two where a lane has one chunk of each.
@@ -311,17 +310,21 @@ int grad_grid(int64_t T, const RowPlan& p) {
 // of dy and a reader of dx 122.0 us instead of 136.2.
 constexpr int64_t kGradStreamBytes = int64_t(160) << 20;
 
-// Whether a batch goes through the one-launch kernel: 512 x 2048 takes 12.1 us
-// a call instead of 17.1, 512 x 8192 (16 MB of dy and z) 12.1 instead of 17.2.
-// The few slices of a dw column make it slow for many rows: 2048 x 2048 would
-// take 21.7 us instead of 17.0, 8000 x 100 64 instead of 19.
+// Whether a batch goes through the one-launch kernel.  Up to 1024 rows and
+// 16 MB of dy and z it does: 512 x 2048 takes 12.1 us a call instead of 17.1,
+// 512 x 8192 12.1 instead of 17.2; the few slices of a dw column make it slow
+// for many rows (2048 x 2048 would take 21.7 us instead of 17.0, 8000 x 100 64
+// instead of 19).  So do rows of more than 16384 columns, for which the other
+// kernel would have more than 16 columns of dw to a lane and one workgroup to
+// a compute unit: 3000 x 20000 in bf16 158 us instead of 345, 1000 x 32768 in
+// 32 bits 180 instead of 228 (at 12288 columns 171 instead of 103).
 constexpr int64_t kSmallRows = 1024, kSmallBytes = int64_t(16) << 20;
-constexpr int kSmallPieces = 32;
+constexpr int kWide = 16384;
 
 template <typename X, typename S>
-bool is_small(int64_t T, int d) {
-  return T <= kSmallRows && T * d * int64_t(sizeof(X) + sizeof(S)) <= kSmallBytes &&
-         pieces_of(d, kCols<X, S>) <= kSmallPieces;
+bool one_launch(int64_t T, int d) {
+  return d > kWide ||
+         (T <= kSmallRows && T * d * int64_t(sizeof(X) + sizeof(S)) <= kSmallBytes);
 }
 
 bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
@@ -330,16 +333,16 @@ bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
 }
 
 template <typename X, typename S, int THREADS, int C>
-void launch_small(const NormGradArgs& args, hipStream_t st) {
+void launch_rows_and_columns(const NormGradArgs& args, hipStream_t st) {
   NormGradArgs a = args;
   const int columns = a.dweight ? (a.d + kSmallCols - 1) / kSmallCols : 0;
   auto launch = [&](int rows, int columns) {
     a.rows = rows;
     if (a.d % kCols<X, S> != 0)
-      rms_norm_backward_small_kernel<X, S, true, THREADS, C>
+      rms_norm_backward_rows_columns_kernel<X, S, true, THREADS, C>
           <<<rows + columns, THREADS, 0, st>>>(a);
     else
-      rms_norm_backward_small_kernel<X, S, false, THREADS, C>
+      rms_norm_backward_rows_columns_kernel<X, S, false, THREADS, C>
           <<<rows + columns, THREADS, 0, st>>>(a);
   };
   // Where dz or dx takes the place of dy or z, dw has to read them first.
@@ -355,7 +358,7 @@ void launch_small(const NormGradArgs& args, hipStream_t st) {
 
 template <typename X, typename S>
 size_t partials(int64_t T, int d) {
-  if (is_small<X, S>(T, d)) return 0;
+  if (one_launch<X, S>(T, d)) return 0;
   size_t rows = 0;
   with_backward_plan<kCols<X, S>>(pieces_of(d, kCols<X, S>), [&](auto plan) {
     const RowPlan p = {decltype(plan)::kWaves, decltype(plan)::kChunks};
@@ -366,16 +369,20 @@ size_t partials(int64_t T, int d) {
 
 template <typename X, typename S>
 hipError_t run_bwd(const NormGradArgs& a, hipStream_t st) {
-  if (is_small<X, S>(a.T, a.d)) {
+  if (one_launch<X, S>(a.T, a.d)) {
     const int pieces = pieces_of(a.d, kCols<X, S>);
     if (pieces <= 4)
-      launch_small<X, S, 256, 1>(a, st);
+      launch_rows_and_columns<X, S, 256, 1>(a, st);
     else if (pieces <= 8)
-      launch_small<X, S, 256, 2>(a, st);
+      launch_rows_and_columns<X, S, 256, 2>(a, st);
     else if (pieces <= 16)
-      launch_small<X, S, 256, 4>(a, st);
-    else
-      launch_small<X, S, 512, 4>(a, st);
+      launch_rows_and_columns<X, S, 256, 4>(a, st);
+    else if (pieces <= 32)
+      launch_rows_and_columns<X, S, 512, 4>(a, st);
+    else if (pieces <= 64)
+      launch_rows_and_columns<X, S, 1024, 4>(a, st);
+    else if constexpr (kCols<X, S> == 4)
+      launch_rows_and_columns<X, S, 1024, 8>(a, st);
     return hipGetLastError();
   }
   with_backward_plan<kCols<X, S>>(pieces_of(a.d, kCols<X, S>), [&](auto plan) {
@@ -413,7 +420,7 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   const int count = static_cast<int>(rms_norm_backward_partials(a.T, a.d, a.bf16, a.stream_bf16));
-  if (!a.dweight || (a.T > 0 && count == 0)) return hipSuccess;  // a small batch has written dw
+  if (!a.dweight || (a.T > 0 && count == 0)) return hipSuccess;  // one launch has written dw
   rms_norm_dweight_kernel<<<(a.d + kSumCols - 1) / kSumCols, kSumCols * kSumSlices, 0, st>>>(
       a.partial, count, a.d, a.dweight);
   return hipGetLastError();

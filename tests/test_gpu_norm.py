@@ -178,7 +178,8 @@ def test_in_place_at_ragged_ends(d, ty):
                                  (700, 767), (1500, 2048), (40, 3001), (5, 8192), (3, 8200),
                                  (2, 32768), (22000, 100), (5000, 511), (6000, 513), (5001, 767),
                                  (1500, 3001), (600, 8192), (300, 8200), (300, 16400), (70, 32768),
-                                 (1000, 2500), (1024, 2048), (1025, 2048), (1000, 1000)])
+                                 (1000, 2500), (1024, 2048), (1025, 2048), (1000, 1000), (400, 16384),
+                                 (400, 12289), (300, 16385), (200, 20001)])
 def test_backward(T, d, ty, st):
     """dz within 64 roundings of its terms' sizes (the dot's chains are the
     sum of squares' above); dw is added over at most ceil(T / 1024) rows (a
