@@ -183,9 +183,9 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void rms_norm_dweight_kernel
 }
 
 // Small batches, and the widest rows, in one launch without a workspace: the
-// first a.rows (T, or none) workgroups have a row of dz each, and the others 32
-// columns of dw, for which they read dy and z once more (dw needs no row's
-// dot).
+// first a.rows workgroups have the rows of dz (all of them, or none), and the
+// others 32 columns of dw each, for which they read dy and z once more (dw
+// needs no row's dot).
 constexpr int kSmallCols = 32;
 
 template <typename X, typename S, bool RAGGED, int THREADS, int C>
@@ -201,38 +201,40 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_rows_columns_kernel
     const S* dres = static_cast<const S*>(a.dresidual);
     S* dz = static_cast<S*>(a.dz);
     X* dx = static_cast<X*>(a.dx);
-    const size_t row = static_cast<size_t>(blockIdx.x) * a.d;
     const float offset = a.weight_offset + (w ? 0.0f : 1.0f);
-    const float rstd = a.rstd[blockIdx.x];
-    Pack<X, V> yr[C], wr[C] = {};
-    Pack<S, V> zr[C], er[C] = {};
+    for (int64_t t = blockIdx.x; t < a.T; t += a.rows) {
+      const size_t row = static_cast<size_t>(t) * a.d;
+      const float rstd = a.rstd[t];
+      Pack<X, V> yr[C], wr[C] = {};
+      Pack<S, V> zr[C], er[C] = {};
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const At at((c * THREADS + threadIdx.x) * V, a.d);
-      at.template load<false>(yr[c], dy + row);
-      at.template load<false>(zr[c], zin + row);
-      if (w) at.template load<false>(wr[c], w);
-      if (dres) at.template load<false>(er[c], dres + row);
-    }
-    float g[C][V], dot = 0.0f;
+      for (int c = 0; c < C; ++c) {
+        const At at((c * THREADS + threadIdx.x) * V, a.d);
+        at.template load<false>(yr[c], dy + row);
+        at.template load<false>(zr[c], zin + row);
+        if (w) at.template load<false>(wr[c], w);
+        if (dres) at.template load<false>(er[c], dres + row);
+      }
+      float g[C][V], dot = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+      for (int c = 0; c < C; ++c) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[c][i] = yr[c].get(i) * (wr[c].get(i) + offset);
-      At((c * THREADS + threadIdx.x) * V, a.d).clear(g[c]);
+        for (int i = 0; i < V; ++i) g[c][i] = yr[c].get(i) * (wr[c].get(i) + offset);
+        At((c * THREADS + threadIdx.x) * V, a.d).clear(g[c]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) dot += g[c][i] * (zr[c].get(i) * rstd);
-    }
-    dot = team_total<THREADS / kWave>(dot, lds) * inv_d;
+        for (int i = 0; i < V; ++i) dot += g[c][i] * (zr[c].get(i) * rstd);
+      }
+      dot = team_total<THREADS / kWave>(dot, lds) * inv_d;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const At at((c * THREADS + threadIdx.x) * V, a.d);
-      float v[V];
+      for (int c = 0; c < C; ++c) {
+        const At at((c * THREADS + threadIdx.x) * V, a.d);
+        float v[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        v[i] = rstd * (g[c][i] - zr[c].get(i) * rstd * dot) + er[c].get(i);
-      at.store(packed<S, V>(v), dz + row);
-      if (dx) at.store(packed<X, V>(v), dx + row);
+        for (int i = 0; i < V; ++i)
+          v[i] = rstd * (g[c][i] - zr[c].get(i) * rstd * dot) + er[c].get(i);
+        at.store(packed<S, V>(v), dz + row);
+        if (dx) at.store(packed<X, V>(v), dx + row);
+      }
     }
     return;
   }
@@ -336,7 +338,7 @@ template <typename X, typename S, int THREADS, int C>
 void launch_rows_and_columns(const NormGradArgs& args, hipStream_t st) {
   NormGradArgs a = args;
   const int columns = a.dweight ? (a.d + kSmallCols - 1) / kSmallCols : 0;
-  auto launch = [&](int rows, int columns) {
+  auto launch = [&](int rows, int columns) {  // workgroups
     a.rows = rows;
     if (a.d % kCols<X, S> != 0)
       rms_norm_backward_rows_columns_kernel<X, S, true, THREADS, C>
@@ -347,12 +349,13 @@ void launch_rows_and_columns(const NormGradArgs& args, hipStream_t st) {
   };
   // Where dz or dx takes the place of dy or z, dw has to read them first.
   const int64_t nx = a.T * a.d * sizeof(X), ns = a.T * a.d * sizeof(S);
+  const int rows = static_cast<int>(a.T < (1 << 20) ? a.T : (1 << 20));
   if (columns > 0 && (overlap(a.dz, ns, a.dy, nx) || overlap(a.dz, ns, a.z, ns) ||
                       overlap(a.dx, nx, a.dy, nx) || overlap(a.dx, nx, a.z, ns))) {
     launch(0, columns);
-    launch(static_cast<int>(a.T), 0);
+    launch(rows, 0);
   } else {
-    launch(static_cast<int>(a.T), columns);
+    launch(rows, columns);
   }
 }
 

@@ -38,7 +38,7 @@ struct NormGradArgs {
   const void* dresidual;
   void *dz, *dx;
   float *dweight, *partial;
-  int rows;  // small batches: workgroups that have a row (set by the launcher)
+  int rows;  // rows and columns in one launch: workgroups of rows (set by the launcher)
 };
 // Rows of d floats in the workspace.
 size_t rms_norm_backward_partials(int64_t T, int d, bool bf16, bool stream_bf16);

@@ -331,6 +331,21 @@ def test_rows_past_32_bits_of_elements():
     close(f64(g.dweight), f64(x[-3:]).sum(axis=0), np.abs(f64(x[-3:])).sum(axis=0) * 400 * O.U32, "dweight")
 
 
+def test_backward_of_more_wide_rows_than_workgroups():
+    """Rows of more than 16384 columns, more of them than one launch has
+    workgroups for rows: the last rows and the columns' sums."""
+    T, d = (1 << 20) + 3, 16400
+    z = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    z[-3:] = randn(np.random.default_rng(1), (3, d), "bf16")
+    w = randn(np.random.default_rng(2), (d,), "bf16")
+    dy, rstd = torch.ones_like(z), torch.ones(T, device=DEV)
+    print("[gpu] rms_norm_backward wide and long", flush=True)
+    g = fff.rms_norm_backward(dy, z, w, rstd, dz=dy)
+    small = fff.rms_norm_backward(torch.ones_like(z[-3:]), z[-3:].clone(), w, rstd[-3:].clone())
+    assert torch.equal(g.dz[-3:], small.dz) and torch.equal(g.dz[0], w) and torch.equal(g.dz[(1 << 20) - 1], w)
+    assert torch.equal(g.dweight, small.dweight)  # every other row adds zeros
+
+
 def test_on_another_stream_and_in_a_graph():
     T, d = 130, 2048
     x, r, w = inputs(T, d, "bf16", "bf16", seed=3)
