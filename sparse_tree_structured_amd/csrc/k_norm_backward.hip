@@ -52,6 +52,7 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_backward_kernel
       gain[c][i] = wr.get(i) + a.weight_offset + (w ? 0.0f : 1.0f);
       acc[c][i] = 0.0f;
     }
+    at.clear(gain[c]);  // zero times an infinite weight would be NaN in the dot
   }
   const int64_t stride = int64_t(gridDim.x) * kRows;
   int set = 0;

@@ -198,6 +198,26 @@ def test_backward(T, d, ty, st):
         assert (o.dx is o.dz) == (ty == st)
 
 
+@pytest.mark.parametrize("ty,st", PAIRS)
+@pytest.mark.parametrize("T,d", [(3, 767), (1100, 5), (1100, 767), (1100, 2047), (1100, 2048),
+                                 (1100, 4099)])
+def test_backward_of_an_infinite_weight(T, d, ty, st):
+    """An infinite weight in the last column makes every row's mean infinite:
+    dz is infinite elsewhere, against the signs of z and of the mean, in both
+    kernels and in every lane, and dw stays finite."""
+    x, _, w = inputs(T, d, ty, st, residual=False)
+    z = torch.where(x == 0, torch.ones_like(x), x)  # no zero times infinity
+    dy = torch.ones(T, d, dtype=TY[ty], device=DEV)
+    w[-1] = float("inf")
+    rstd = torch.rsqrt((z.float() ** 2).mean(1) + 1e-6)
+    print(f"[gpu] rms_norm_backward of an infinite weight T={T} d={d} {ty} {st}", flush=True)
+    g = fff.rms_norm_backward(dy, z, w, rstd)
+    got, s = f64(g.dz)[:, :-1], np.sign(f64(z))
+    want = -s[:, :-1] * s[:, -1:] * np.inf
+    assert (got == want).all()
+    assert torch.isfinite(g.dweight).all()
+
+
 def test_backward_against_differences_of_the_forward():
     """d/dh of sum(y dy) + sum(z dres) along random directions, from the
     library's own float32 forward: central differences with h = 2^-6 have a
