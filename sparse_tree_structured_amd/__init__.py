@@ -606,8 +606,17 @@ class RmsNormGrad(NamedTuple):
     dweight: object  # [d] float32
 
 
-# Descriptors of sizes the library only reads: one for each set of values.
-_norm_shape = functools.lru_cache(maxsize=256)(NormShape)
+@functools.lru_cache(maxsize=256)
+def _norm_shape(T, d, dtype, stream_dtype, out_dtype, group, eps, weight_offset) -> NormShape:
+    """The descriptor of these sizes, which the library only reads: one for
+    each set of values.  ctypes cuts a number that its field cannot hold, and
+    the library would see another size than the tensors have."""
+    s = NormShape(T, d, dtype, stream_dtype, out_dtype, group, eps, weight_offset)
+    if s.d != d:
+        raise FFFError(ERROR_NOT_SUPPORTED, f"norm of rows of {d} columns")
+    if s.group != group:
+        raise FFFError(ERROR_INVALID_VALUE, f"norm with group {group}")
+    return s
 
 
 class _Torch:
@@ -709,6 +718,7 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
     e4m3 = out_ty is rt.f8
     if not e4m3 and out_ty is not ty:
         raise ValueError(f"y must be {ty} or {rt.f8}, got {out_ty}")
+    sizes = _norm_shape(T, d, code, stream_code, DTYPE_E4M3 if e4m3 else code, group, eps, weight_offset)
     handle = _here(rt, x, stream)
     if residual is None and stream_ty is not ty:  # x is the stream itself
         px, pr = 0, px
@@ -736,9 +746,7 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
             ps = scale.data_ptr()
     elif scale is not None:
         raise ValueError(f"scale is for a y of {rt.f8}")
-    st = (_lib or load_library()).fff_rms_norm(
-        _norm_shape(T, d, code, stream_code, DTYPE_E4M3 if e4m3 else code, group, eps, weight_offset),
-        px, pr, pw, py, ps, pz, prs, handle)
+    st = (_lib or load_library()).fff_rms_norm(sizes, px, pr, pw, py, ps, pz, prs, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_rms_norm")
     return RmsNorm(y, residual_out, rstd, scale)
@@ -749,7 +757,7 @@ def rms_norm_backward_workspace_size(T: int, d: int, dtype: int, stream_dtype: i
     """Workspace bytes of rms_norm_backward (dtypes: fff_dtype_t codes)."""
     n = ctypes.c_size_t()
     st = load_library().fff_rms_norm_backward_workspace_size(
-        NormShape(T, d, dtype, stream_dtype, dtype, 0, 0.0, 0.0), ctypes.byref(n))
+        _norm_shape(T, d, dtype, stream_dtype, dtype, 0, 0.0, 0.0), ctypes.byref(n))
     if st != SUCCESS:
         raise FFFError(st, "fff_rms_norm_backward_workspace_size")
     return n.value
@@ -775,6 +783,7 @@ def rms_norm_backward(dy, z, weight, rstd, *, dresidual=None, weight_offset: flo
     pr = _tensor(rstd, (T,), f32, dy, "rstd [T]")
     pe = _tensor(dresidual, shape, zty, dy, "dresidual") if dresidual is not None else 0
     code, zcode = _code(rt, ty), _code(rt, zty)
+    sizes = _norm_shape(T, d, code, zcode, code, 0, 0.0, weight_offset)
     handle = _here(rt, dy, stream)
     pdx = pdw = pws = have = 0
     if dz is not None:
@@ -801,8 +810,7 @@ def rms_norm_backward(dy, z, weight, rstd, *, dresidual=None, weight_offset: flo
             workspace = _empty(rt, (have,), rt.u8, dy.device, stream)
             pws = workspace.data_ptr()
     st = (_lib or load_library()).fff_rms_norm_backward(
-        _norm_shape(T, d, code, zcode, code, 0, 0.0, weight_offset), pdy, pz, pw, pr, pe, pdz, pdx,
-        pdw, pws, have, handle)
+        sizes, pdy, pz, pw, pr, pe, pdz, pdx, pdw, pws, have, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_rms_norm_backward")
     return RmsNormGrad(dz, dz if dx is None else dx, dweight)
