@@ -490,9 +490,11 @@ fff_status_t fff_rms_norm_backward(const fff_norm_shape_t *shape, const void *dy
  * with lr = config.lr * lr_scale of the tensor.  Every product, sum, quotient
  * and root is rounded to 32 bits on its own, in this order, so that the step
  * gives the same bits wherever it runs.  Tensors are updated in place, many
- * to a launch; no two that are written may overlap.  A gradient that is not
- * finite makes its own element so (and where it is infinite its block of an
- * 8-bit state); fff_grad_norm and grad_scale leave such a step out.
+ * to a launch; no two that are written (scales among them) may overlap, and
+ * no gradient may overlap one that is, but for a buffer of its own entry and
+ * of its type.  A gradient that is not finite makes its own element so (and
+ * where it is infinite its block of an 8-bit state); fff_grad_norm and
+ * grad_scale leave such a step out.
  *
  * State in 32 bits (state_dtype F32): exp_avg holds m, exp_avg_sq v.
  * State in 8 bits (E4M3): exp_avg holds m and exp_avg_sq holds sqrt(v), each

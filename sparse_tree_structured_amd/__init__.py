@@ -8,6 +8,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
 import os
@@ -873,6 +874,35 @@ def grad_table(grads) -> TensorTable:
     return TensorTable(entries, grads[0], None, grads)
 
 
+def _check_apart(entries, e4m3):
+    """Refuses a table whose step would write some memory twice, or read a
+    gradient where it writes: workgroups run in any order.  A gradient may be
+    a buffer of its own entry, whose elements a lane reads before it writes."""
+    size = {DTYPE_F32: 4, DTYPE_BF16: 2}
+    state = 1 if e4m3 else 4
+    written, grads = [], []
+    for i, e in enumerate(entries):
+        blocks = -(-e.n // ADAMW_BLOCK)
+        for name, at, n in (("params", e.param, e.n * size[e.param_dtype]), ("masters", e.master, e.n * 4),
+                            ("exp_avg", e.exp_avg, e.n * state), ("exp_avg_sq", e.exp_avg_sq, e.n * state),
+                            ("scales", e.scale, blocks * 8)):
+            if at and n:
+                written.append((at, at + n, i, name))
+        if e.n:
+            grads.append((e.grad, e.grad + e.n * size[e.grad_dtype], i))
+    written.sort()
+    for (_, end, i, a), (start, _, j, b) in zip(written, written[1:]):
+        if start < end:
+            raise ValueError(f"{a}[{i}] and {b}[{j}] share memory: every param, master, state and scale "
+                             "must be its own")
+    starts = [w[0] for w in written]
+    for start, end, i in grads:
+        # the last written one that starts before the gradient ends: none before it reaches further
+        k = bisect.bisect_left(starts, end) - 1
+        if k >= 0 and written[k][1] > start and written[k][:3] != (start, end, i):
+            raise ValueError(f"grads[{i}] and {written[k][3]}[{written[k][2]}] share memory")
+
+
 def adamw_state(params, bits: int = 32):
     """The state before the first step, as adamw_table takes it: lists
     (exp_avg, exp_avg_sq, scales), float32, or for ``bits`` = 8 float8_e4m3fn
@@ -896,7 +926,8 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
     of one dtype (float32, or float8_e4m3fn with ``scales``; adamw_state makes
     them).  ``masters``: float32 masters of bf16 params (None, or a list with
     None where a param has none).  ``weight_decay`` and ``lr_scale``: one
-    number, or one for each tensor."""
+    number, or one for each tensor.  No two tensors that a step writes may
+    share memory."""
     torch = _torch()
     params = list(params)
     n = len(params)
@@ -930,9 +961,7 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
         if e4m3:
             e.scale = _flat(sc, 2 * -(-e.n // ADAMW_BLOCK), f32, dev, f"scales[{i}]")
         e.lr_scale, e.weight_decay = float(shares[i]), float(decays[i])
-    written = [q for e in entries if e.n for q in (e.param, e.master, e.exp_avg, e.exp_avg_sq) if q]
-    if len(set(written)) != len(written):
-        raise ValueError("a tensor is in the table twice: every param, master and state must be its own")
+    _check_apart(entries, e4m3)
     return TensorTable(entries, params[0], DTYPE_E4M3 if e4m3 else DTYPE_F32, (params, lists))
 
 

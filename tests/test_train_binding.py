@@ -72,3 +72,80 @@ def test_a_group_that_fits_its_field_is_the_librarys_to_refuse():
         s = fff._norm_shape(4, 300, fff.DTYPE_BF16, fff.DTYPE_BF16, fff.DTYPE_E4M3, group, 1e-6, 0.0)
         assert s.group == group
         assert fff.load_library().fff_rms_norm(s, *[0x10000] * 7, None) == fff.ERROR_INVALID_VALUE
+
+
+# ---- the optimiser's table ----
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """Tables of CPU tensors: nothing steps them."""
+    def flat(t, n, dtypes, device, what):
+        assert t.numel() == n and t.dtype in dtypes and t.is_contiguous()
+        return t.data_ptr()
+    monkeypatch.setattr(fff, "_flat", flat)
+
+
+def tensors(n=300, count=2, bits=8, dtype=B):
+    p, g = ([torch.zeros(n, dtype=dtype) for _ in range(count)] for _ in range(2))
+    m, v, s = fff.adamw_state(p, bits)
+    w = [torch.zeros(n) for _ in range(count)] if dtype is B else None
+    return dict(params=p, grads=g, exp_avg=m, exp_avg_sq=v, masters=w, scales=s)
+
+
+def table(t):
+    t = dict(t)
+    return fff.adamw_table(t.pop("params"), t.pop("grads"), t.pop("exp_avg"), t.pop("exp_avg_sq"), **t)
+
+
+@pytest.mark.parametrize("key", ["params", "masters", "exp_avg", "exp_avg_sq", "scales"])
+def test_a_tensor_that_two_entries_write_is_refused(on_cpu, key):
+    t = tensors()
+    assert table(t).count == 2
+    t[key][1] = t[key][0]
+    with pytest.raises(ValueError, match=rf"{key}\[0\] and {key}\[1\]"):
+        table(t)
+
+
+@pytest.mark.parametrize("key,over", [("params", 1), ("masters", 1), ("exp_avg", 1), ("exp_avg_sq", 299),
+                                      ("scales", 2)])
+def test_views_that_share_some_elements_are_refused(on_cpu, key, over):
+    t = tensors()
+    n = t[key][0].numel()
+    buf = torch.zeros(2 * n, dtype=torch.uint8 if t[key][0].dtype is F8 else t[key][0].dtype).view(t[key][0].dtype)
+    shape = t[key][0].shape
+    t[key] = [buf[:n].view(shape), buf[n:].view(shape)]  # side by side
+    table(t)
+    t[key] = [buf[over:n + over].view(shape), buf[:n].view(shape)]
+    with pytest.raises(ValueError, match=rf"{key}\[1\] and {key}\[0\] share memory"):
+        table(t)
+
+
+def test_lists_that_share_a_tensor_are_refused(on_cpu):
+    t = tensors(dtype=torch.float32, bits=32)
+    t["exp_avg_sq"] = t["exp_avg"]
+    with pytest.raises(ValueError, match="exp_avg"):
+        table(t)
+
+
+def test_a_gradient_in_memory_that_another_tensor_writes_is_refused(on_cpu):
+    """A lane reads its gradient before it writes its own elements, but other
+    workgroups may have written another's."""
+    t = tensors(dtype=torch.float32, bits=32)
+    t["grads"][1] = t["grads"][0]  # only read: no harm
+    table(t)
+    t["grads"][0] = t["params"][0]  # element by element its own
+    table(t)
+    t["grads"][0] = t["params"][1]
+    with pytest.raises(ValueError, match=r"grads\[0\] and params\[1\] share memory"):
+        table(t)
+    buf = torch.zeros(301)
+    t["grads"][0], t["params"][0] = buf[:300], buf[1:]
+    with pytest.raises(ValueError, match=r"grads\[0\] and params\[0\] share memory"):
+        table(t)
+
+
+def test_empty_tensors_share_nothing(on_cpu):
+    t = tensors(dtype=torch.float32, bits=32)
+    for key in ("params", "grads", "exp_avg", "exp_avg_sq"):
+        t[key].append(t["params"][0][:0])
+    assert table(t).count == 3
