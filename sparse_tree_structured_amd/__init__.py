@@ -861,6 +861,17 @@ def _listed(values, n, what):
     return values
 
 
+def _tensors(values, n, what, torch):
+    """A list of n tensors; None is n of them."""
+    if values is None:
+        return [None] * n
+    # A tensor would list its rows; two entries must not share one.
+    values = [values] if isinstance(values, torch.Tensor) else list(values)
+    if len(values) != n:
+        raise ValueError(f"{what} must have one entry for each of {n} tensors, got {len(values)}")
+    return values
+
+
 def grad_table(grads) -> TensorTable:
     """A table of gradients alone, for grad_norm."""
     torch = _torch()
@@ -937,7 +948,7 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
     f32, both = (torch.float32,), (torch.float32, torch.bfloat16)
     lists = {"grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
              "masters": masters, "scales": scales}
-    lists = {k: _listed(v, n, k) for k, v in lists.items()}
+    lists = {k: _tensors(v, n, k, torch) for k, v in lists.items()}
     decays, shares = _listed(weight_decay, n, "weight_decay"), _listed(lr_scale, n, "lr_scale")
     state = (lists["exp_avg"][0].dtype,)
     e4m3 = state[0] == torch.float8_e4m3fn

@@ -149,3 +149,14 @@ def test_empty_tensors_share_nothing(on_cpu):
     for key in ("params", "grads", "exp_avg", "exp_avg_sq"):
         t[key].append(t["params"][0][:0])
     assert table(t).count == 3
+
+
+@pytest.mark.parametrize("key", ["grads", "exp_avg", "exp_avg_sq", "masters", "scales"])
+def test_one_tensor_is_not_every_entrys(on_cpu, key):
+    t = tensors()
+    t[key] = t[key][0]
+    with pytest.raises(ValueError, match="one entry for each"):
+        table(t)
+    one = {k: v[:1] for k, v in tensors().items()}
+    one[key] = one[key][0]  # the only entry's
+    assert table(one).count == 1
