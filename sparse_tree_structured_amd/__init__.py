@@ -919,6 +919,7 @@ def adamw_state(params, bits: int = 32):
     (exp_avg, exp_avg_sq, scales), float32, or for ``bits`` = 8 float8_e4m3fn
     with scales [blocks, 2] (else None)."""
     torch = _torch()
+    params = list(params)
     if bits not in (8, 32):
         raise ValueError(f"bits must be 8 or 32, got {bits}")
     if bits == 32:

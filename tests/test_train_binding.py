@@ -160,3 +160,14 @@ def test_one_tensor_is_not_every_entrys(on_cpu, key):
     one = {k: v[:1] for k, v in tensors().items()}
     one[key] = one[key][0]  # the only entry's
     assert table(one).count == 1
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_state_of_parameters_that_can_be_walked_once(on_cpu, bits):
+    """Module.parameters() is a generator."""
+    module = torch.nn.Linear(30, 20)
+    m, v, s = fff.adamw_state(module.parameters(), bits)
+    assert [t.shape for t in m] == [t.shape for t in v] == [(20, 30), (20,)]
+    assert s is None if bits == 32 else [tuple(t.shape) for t in s] == [(5, 2), (1, 2)]
+    grads = (torch.zeros_like(p) for p in module.parameters())
+    assert fff.adamw_table(module.parameters(), grads, m, v, scales=s).count == 2
