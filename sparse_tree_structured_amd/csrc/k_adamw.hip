@@ -101,7 +101,9 @@ __device__ __forceinline__ float short_div(float m, float d) {
   return __builtin_fmaf(__builtin_fmaf(-q, d, m), y, q);
 }
 
-// The ranges' ends: 2 bits(m) - 1 and bits(v) - 1 (zero wraps to the top).
+// The ranges' ends: 2 bits(m) - 1 and bits(v) - 1 (zero wraps to the top).  A
+// root below 2^30 over sqrt(1 - beta2^t), which is above 2^-27 for every beta2
+// below 1, and an eps inside its ends give a divisor in the quotient's range.
 constexpr uint32_t kShortLowM = 2 * (67u << 23) - 1;  // 2^-60
 constexpr uint32_t kShortLowV = (37u << 23) - 1;      // 2^-90
 constexpr float kShortTop = 0x1p60f;
@@ -182,7 +184,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
       top_v = fmaxf(top_v, v[i]);
     }
     if (low_m < kShortLowM || low_v < kShortLowV || !(top_m < kShortTop && top_v < kShortTop) ||
-        a.eps < kShortEps) {
+        !(a.eps >= kShortEps && a.eps < kShortTop)) {
       top_r = 0.0f;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {

@@ -1,0 +1,49 @@
+"""The norm and the optimiser at the ends of their arguments' ranges, on the
+GPU: AdamW bit for bit with its formulas evaluated operation by operation in
+32 bits."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_tree_structured_amd as fff
+import train_oracle as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+KW = dict(lr=1.0, beta1=0.9, beta2=0.99)
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def same(got, want, what):
+    got = got.cpu().numpy()
+    eq = (got == want) | (np.isnan(got) & np.isnan(want))
+    assert eq.all(), f"{what}: {(~eq).sum()} of {eq.size} differ"
+
+
+def step_of(p, g, m, v, **kw):
+    """A step on the GPU and the same by the formulas: (tensors, oracle)."""
+    with np.errstate(all="ignore"):
+        o = O.adamw(p, g, m, v, wd=0.0, step=3, **kw)
+    t = [dev(a) for a in (p, g, m, v)]
+    fff.adamw_step(fff.adamw_table([t[0]], [t[1]], [t[2]], [t[3]]), step=3, **kw)
+    return t, o
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -60, 2.0 ** 59, 2.0 ** 60, 2.0 ** 90, 1e30, 2.0 ** 126, 3e38, 1e39])
+def test_an_eps_of_any_size(eps):
+    """Weights of zero show the quotient's own bits.  The last eps is infinite
+    in 32 bits: the quotient is zero."""
+    print(f"[gpu] adamw eps={eps}", flush=True)
+    rng = np.random.default_rng(21)
+    n = 4096
+    size = 2.0 ** rng.uniform(-60, 59, n)
+    g = (rng.normal(size=n) * np.minimum(size, 2.0 ** 28)).astype(np.float32)
+    m = (rng.normal(size=n) * size).astype(np.float32)
+    t, o = step_of(np.zeros(n, np.float32), g, m, rng.random(n).astype(np.float32), eps=eps, **KW)
+    same(t[0], o["p"], "param")
+    same(t[2], o["m"], "exp_avg")
+    same(t[3], o["v"], "exp_avg_sq")
+    assert np.isfinite(o["p"]).all()
