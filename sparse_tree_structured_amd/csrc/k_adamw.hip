@@ -107,6 +107,7 @@ __device__ __forceinline__ float short_div(float m, float d) {
 constexpr uint32_t kShortLowM = 2 * (67u << 23) - 1;  // 2^-60
 constexpr uint32_t kShortLowV = (37u << 23) - 1;      // 2^-90
 constexpr float kShortTop = 0x1p60f;
+constexpr uint32_t kShortTopV = 187u << 23;           // 2^60
 constexpr float kShortEps = 0x1p-60f;
 
 __device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
@@ -169,7 +170,8 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
     // this lane is zero or in their range, which is all but always.
     float v[kV], ratio[kV];
     uint32_t low_m = ~0u, low_v = ~0u;  // smallest sizes above zero, zero as the largest
-    float top_m = 0.0f, top_r = 0.0f, top_v = 0.0f;
+    uint32_t top_v = 0;  // as bits: NaN and anything below zero are above every number
+    float top_m = 0.0f, top_r = 0.0f;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const float g = q[k].g.get(i) * gs;
@@ -181,9 +183,9 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
       low_v = umin(low_v, __float_as_uint(v[i]) - 1);
       top_m = fmaxf(top_m, fabsf(m[i]));
       top_r = fmaxf(top_r, r[i]);
-      top_v = fmaxf(top_v, v[i]);
+      top_v = umax(top_v, __float_as_uint(v[i]));
     }
-    if (low_m < kShortLowM || low_v < kShortLowV || !(top_m < kShortTop && top_v < kShortTop) ||
+    if (low_m < kShortLowM || low_v < kShortLowV || !(top_m < kShortTop) || top_v >= kShortTopV ||
         !(a.eps >= kShortEps && a.eps < kShortTop)) {
       top_r = 0.0f;
 #pragma unroll

@@ -47,3 +47,20 @@ def test_an_eps_of_any_size(eps):
     same(t[2], o["m"], "exp_avg")
     same(t[3], o["v"], "exp_avg_sq")
     assert np.isfinite(o["p"]).all()
+
+
+@pytest.mark.parametrize("bad", [-(2.0 ** -126), -1e-20, -1.0, -1e30, float("nan"), float("-inf")])
+def test_a_second_moment_below_zero_is_not_hidden(bad):
+    """No step makes one; a damaged state's element becomes NaN, as the root
+    of a negative number is, and the others stay as they are."""
+    print(f"[gpu] adamw exp_avg_sq={bad}", flush=True)
+    rng = np.random.default_rng(22)
+    n = 600
+    p, m = (rng.normal(size=n).astype(np.float32) for _ in range(2))
+    v = rng.random(n).astype(np.float32)
+    v[::7] = bad
+    t, o = step_of(p, np.zeros(n, np.float32), m, v, eps=1e-8, **KW)
+    assert np.isnan(o["p"][::7]).all() and np.isfinite(np.delete(o["p"], np.s_[::7])).all()
+    same(t[0], o["p"], "param")
+    same(t[2], o["m"], "exp_avg")
+    same(t[3], o["v"], "exp_avg_sq")
