@@ -224,6 +224,7 @@ fff_status_t fff_adamw_step(const fff_adamw_config_t* config, const fff_adamw_te
   a.beta2 = static_cast<float>(c.beta2);
   a.one_beta2 = static_cast<float>(1.0 - c.beta2);
   a.eps = static_cast<float>(c.eps);
+  a.long_m = fff::adamw_long_m(a.eps);
   a.root = static_cast<float>(1.0 / sqrt(1.0 - pow(c.beta2, static_cast<double>(c.step))));
   a.grad_scale = c.grad_scale;
   const double bias1 = 1.0 - pow(c.beta1, static_cast<double>(c.step));

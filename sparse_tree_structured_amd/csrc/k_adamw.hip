@@ -101,14 +101,11 @@ __device__ __forceinline__ float short_div(float m, float d) {
   return __builtin_fmaf(__builtin_fmaf(-q, d, m), y, q);
 }
 
-// The ranges' ends: 2 bits(m) - 1 and bits(v) - 1 (zero wraps to the top).  A
-// root below 2^30 over sqrt(1 - beta2^t), which is above 2^-27 for every beta2
-// below 1, and an eps inside its ends give a divisor in the quotient's range.
-constexpr uint32_t kShortLowM = 2 * (67u << 23) - 1;  // 2^-60
-constexpr uint32_t kShortLowV = (37u << 23) - 1;      // 2^-90
+// The ranges' ends as bits(v) - 1 (zero wraps to the top) and bits(v); m's
+// lower end is in AdamwArgs::long_m.
+constexpr uint32_t kShortLowV = (37u << 23) - 1;  // 2^-90
+constexpr uint32_t kShortTopV = 187u << 23;       // 2^60
 constexpr float kShortTop = 0x1p60f;
-constexpr uint32_t kShortTopV = 187u << 23;           // 2^60
-constexpr float kShortEps = 0x1p-60f;
 
 __device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
@@ -185,8 +182,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwEntry
       top_r = fmaxf(top_r, r[i]);
       top_v = umax(top_v, __float_as_uint(v[i]));
     }
-    if (low_m < kShortLowM || low_v < kShortLowV || !(top_m < kShortTop) || top_v >= kShortTopV ||
-        !(a.eps >= kShortEps && a.eps < kShortTop)) {
+    if (low_m <= a.long_m || low_v < kShortLowV || !(top_m < kShortTop) || top_v >= kShortTopV) {
       top_r = 0.0f;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {

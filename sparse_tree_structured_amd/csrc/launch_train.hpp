@@ -79,12 +79,23 @@ constexpr int kFirstBits = 24;  // workgroups of a launch: below 2^24
 struct AdamwArgs {
   float beta1, one_beta1, beta2, one_beta2, eps, root;  // root: 1 / sqrt(1 - beta2^t)
   const float* grad_scale;
+  uint32_t long_m;  // adamw_long_m(eps)
   int count;
   // Each tensor's first workgroup (24 bits) and, above it, its n >> 32.
   uint32_t first[kAdamwMaxTensors];
   AdamwEntry e[kAdamwMaxTensors];
 };
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
+
+// The largest 2 bits(m) - 1 (zero wraps to the top) that needs the long
+// quotient m / (sqrt(v) / sqrt(1 - beta2^t) + eps): the short one is for
+// m = 0 and m from 2^-60 on, over divisors in [2^-60, 2^90).  A root in its
+// own short range is below 2^30 and 1 / sqrt(1 - beta2^t) below 2^27 for
+// every beta2 below 1, so eps in [2^-60, 2^60) gives such a divisor; beside
+// any other every m takes the long quotient.
+constexpr uint32_t adamw_long_m(float eps) {
+  return eps >= 0x1p-60f && eps < 0x1p60f ? 2 * (67u << 23) - 2 : ~0u;
+}
 
 enum AdamwParam { kParamF32 = 0, kParamBf16 = 1, kParamMaster = 2 };
 
