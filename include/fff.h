@@ -423,7 +423,8 @@ fff_status_t fff_forward_static(const fff_shape_t *shape, const fff_plan_t *plan
  *   y    = z * rstd * (weight + weight_offset)
  * y is formed from the 32-bit z; residual_out holds z rounded to
  * stream_dtype.  The squares are summed in 32 bits: a row whose sum leaves
- * their range (values beyond about 1e18) has rstd 0.
+ * their range (values beyond about 1e18) has rstd 0, and with eps 0 a row
+ * whose squares all are below it (values under about 1e-23) rstd infinity.
  *
  * With out_dtype FFF_DTYPE_E4M3, y is held in 8 bits: for every row (group
  * 0) or every `group` columns of a row (32, 64 or 128; the last group may be

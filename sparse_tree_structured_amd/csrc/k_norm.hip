@@ -95,6 +95,8 @@ __global__ __launch_bounds__(block_threads(WAVES)) void rms_norm_kernel(NormArgs
         At((c * kTeam + lane) * V, a.d).clear(z[c]);
 #pragma unroll
         for (int i = 0; i < V; ++i) top[c] = umax(top[c], size_bits(z[c][i]));
+        // (a lane past the row's end: an infinite rstd has made its zeros NaN)
+        if ((c * kTeam + lane) * V >= a.d) top[c] = 0;
       }
       if (a.group == 0) {
 #pragma unroll

@@ -64,3 +64,21 @@ def test_a_second_moment_below_zero_is_not_hidden(bad):
     same(t[0], o["p"], "param")
     same(t[2], o["m"], "exp_avg")
     same(t[3], o["v"], "exp_avg_sq")
+
+
+@pytest.mark.parametrize("ty", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("d", [1, 8, 30, 96, 104, 256, 264, 512, 1000, 1001, 2040])
+def test_an_infinite_rstd_gives_infinite_scales_at_every_width(d, group, ty):
+    """With eps 0, squares too small for 32 bits leave rstd infinite, and with
+    it every output and every scale, whatever lanes the row's end leaves
+    idle.  A row of zeros is 0 times infinity: NaN."""
+    x = torch.full((3, d), 1e-30, dtype=ty, device=DEV)
+    x[1] = 0.0
+    x[2] = 1.0
+    print(f"[gpu] rms_norm rstd=inf d={d} group={group} {ty}", flush=True)
+    o = fff.rms_norm(x, out_dtype=torch.float8_e4m3fn, group=group, eps=0.0, want_rstd=True)
+    assert torch.isinf(o.rstd[:2]).all() and o.rstd[2] == 1.0
+    assert torch.isinf(o.scale[0]).all() and torch.isnan(o.scale[1]).all()
+    assert torch.isnan(o.y[:2].float()).all()
+    assert (o.scale[2] == np.float32(1) / np.float32(448)).all() and (o.y[2].float() == 448).all()
