@@ -452,8 +452,9 @@ typedef struct fff_norm_shape {
  *   scale         [T, ceil(d / group)] float32 ([T] with group 0); E4M3 only
  *   residual_out  [T,d] stream_dtype, or NULL
  *   rstd          [T] float32 for the backward pass, or NULL
- * residual_out may be the residual's own buffer, and any output may be the
- * buffer of an input of its type; other overlaps are not allowed.  One
+ * y and residual_out may each be the buffer of x or of the residual, where it
+ * has their type (residual_out the residual's own, above all); no other
+ * overlap is allowed: every row reads weight while others are written.  One
  * launch; T = 0 is a no-op.
  */
 fff_status_t fff_rms_norm(const fff_norm_shape_t *shape, const void *x, const void *residual,
@@ -473,9 +474,11 @@ fff_status_t fff_rms_norm(const fff_norm_shape_t *shape, const void *x, const vo
  *   dx         [T,d] dtype out: dz rounded to the layer's type, or NULL
  *   dweight    [d] float32 out, or NULL
  * Rows are summed in a fixed order: results are the same on every call.  dz
- * and dx may be the buffers of inputs of their types.  T = 0 gives dweight 0.
- * The workspace is for dweight: without it, or where its size is 0 (small
- * batches), it may be NULL.
+ * and dx may each be the buffer of dy, z or dresidual, where it has their
+ * type; no other overlap is allowed (dweight is not weight's buffer, nor dz
+ * that of rstd where d is 1).  T = 0 gives dweight 0.  The workspace
+ * is for dweight: without it, or where its size is 0 (small batches), it may
+ * be NULL.
  */
 fff_status_t fff_rms_norm_backward_workspace_size(const fff_norm_shape_t *shape, size_t *bytes);
 fff_status_t fff_rms_norm_backward(const fff_norm_shape_t *shape, const void *dy, const void *z,
