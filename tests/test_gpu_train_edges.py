@@ -82,3 +82,68 @@ def test_an_infinite_rstd_gives_infinite_scales_at_every_width(d, group, ty):
     assert torch.isinf(o.scale[0]).all() and torch.isnan(o.scale[1]).all()
     assert torch.isnan(o.y[:2].float()).all()
     assert (o.scale[2] == np.float32(1) / np.float32(448)).all() and (o.y[2].float() == 448).all()
+
+
+# One launch for rows and columns; two; rows and columns in one again past 16384 columns.  Even and odd widths.
+OVER = [(40, 770), (3, 2048), (900, 333), (5000, 770), (3000, 2049), (60, 16400), (50, 16387)]
+
+
+@pytest.mark.parametrize("T,d", OVER)
+def test_backward_of_a_32_bit_stream_over_its_inputs(T, d):
+    """dx in the place of dy, and dz in that of z or of the residual's
+    gradient, one and all of them at once: the same bits, dweight (which other
+    workgroups sum from dy and z) too."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(T + d)
+    z, dres = (torch.randn(T, d, generator=gen, device=DEV) for _ in range(2))
+    dy, w = (torch.randn(*s, generator=gen, device=DEV).bfloat16() for s in ((T, d), (d,)))
+    rstd = fff.rms_norm(z, w, want_rstd=True).rstd
+    print(f"[gpu] rms_norm_backward over its inputs T={T} d={d}", flush=True)
+    want = fff.rms_norm_backward(dy, z, w, rstd, dresidual=dres)
+    assert want.dx.dtype == torch.bfloat16 and want.dz.dtype == torch.float32
+    assert torch.equal(want.dx, want.dz.bfloat16())
+    for over_dy, over in ((True, None), (False, "z"), (True, "z"), (True, "dres"), (False, "dres")):
+        t = dict(dy=dy.clone(), z=z.clone(), dres=dres.clone())
+        g = fff.rms_norm_backward(t["dy"], t["z"], w, rstd, dresidual=t["dres"], dx=t["dy"] if over_dy else None,
+                                  dz=t[over] if over else None)
+        assert not over_dy or g.dx.data_ptr() == t["dy"].data_ptr()
+        assert not over or g.dz.data_ptr() == t[over].data_ptr()
+        assert torch.equal(g.dx, want.dx) and torch.equal(g.dz, want.dz) and torch.equal(g.dweight, want.dweight)
+
+
+@pytest.mark.parametrize("ty", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,d", [(40, 770), (5000, 770), (60, 16400)])
+def test_backward_with_dx_and_dz_of_one_type(T, d, ty):
+    """Both asked for where the types agree: equal, over the inputs too."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(T * d)
+    dy, z = (torch.randn(T, d, generator=gen, device=DEV).to(ty) for _ in range(2))
+    rstd = fff.rms_norm(z, want_rstd=True).rstd
+    print(f"[gpu] rms_norm_backward dx beside dz T={T} d={d} {ty}", flush=True)
+    want = fff.rms_norm_backward(dy, z, None, rstd)
+    for swap in (False, True):
+        a, b = dy.clone(), z.clone()
+        g = fff.rms_norm_backward(a, b, None, rstd, dx=b if swap else a, dz=a if swap else b)
+        assert torch.equal(a, want.dz) and torch.equal(b, want.dz) and torch.equal(g.dweight, want.dweight)
+
+
+@pytest.mark.parametrize("T,d", [(5000, 770), (3000, 2049), (40, 770)])
+def test_backward_with_a_given_workspace(T, d):
+    """Its size as the query says, dirty, and nothing behind it touched."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(T - d)
+    dy, z = (torch.randn(T, d, generator=gen, device=DEV) for _ in range(2))
+    w = torch.randn(d, generator=gen, device=DEV)
+    rstd = fff.rms_norm(z, w, want_rstd=True).rstd
+    need = fff.rms_norm_backward_workspace_size(T, d, fff.DTYPE_F32, fff.DTYPE_F32)
+    assert (need > 0) == (T > 1024)
+    want = fff.rms_norm_backward(dy, z, w, rstd)
+    print(f"[gpu] rms_norm_backward workspace T={T} d={d}", flush=True)
+    buf = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    g = fff.rms_norm_backward(dy, z, w, rstd, workspace=buf[:need])
+    assert torch.equal(g.dz, want.dz) and torch.equal(g.dweight, want.dweight)
+    assert bool((buf[need:] == 0xFF).all())
+    if need:
+        with pytest.raises(fff.FFFError) as e:
+            fff.rms_norm_backward(dy, z, w, rstd, workspace=buf[:need - 1])
+        assert e.value.status == fff.ERROR_WORKSPACE
