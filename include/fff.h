@@ -489,16 +489,22 @@ fff_status_t fff_rms_norm_backward(const fff_norm_shape_t *shape, const void *dy
 /*
  * AdamW (decoupled weight decay) over any number of tensors:
  *   g = grad * grad_scale
- *   m = beta1 m + (1 - beta1) g           v = beta2 v + (1 - beta2) g^2
- *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
- * with lr = config.lr * lr_scale of the tensor.  Every product, sum, quotient
- * and root is rounded to 32 bits on its own, in this order, so that the step
- * gives the same bits wherever it runs.  Tensors are updated in place, many
- * to a launch; no two that are written (scales among them) may overlap, and
- * no gradient may overlap one that is, but for a buffer of its own entry and
- * of its type.  A gradient that is not finite makes its own element so (and
- * where it is infinite its block of an 8-bit state); fff_grad_norm and
- * grad_scale leave such a step out.
+ *   m = m * beta1 + g * (1 - beta1)
+ *   v = v * beta2 + (g * g) * (1 - beta2)
+ *   p = p * decay - step_size * (m / (sqrt(v) * root + eps))
+ * where, with lr = config.lr * lr_scale of the tensor,
+ *   decay = 1 - lr * weight_decay
+ *   step_size = lr / (1 - beta1^step)
+ *   root = 1 / sqrt(1 - beta2^step)
+ * These three, both betas, 1 - beta1, 1 - beta2 and eps are formed in 64 bits
+ * and rounded to 32 once; every product, sum, quotient and root of the four
+ * lines is rounded to 32 bits on its own, in the order written (without
+ * grad_scale, g is grad), so that the step gives the same bits wherever it
+ * runs.  Tensors are updated in place, many to a launch; no two that are
+ * written (scales among them) may overlap, and no gradient may overlap one
+ * that is, but for a buffer of its own entry and of its type.  A gradient that
+ * is not finite makes its own element so (and where it is infinite its block
+ * of an 8-bit state); fff_grad_norm and grad_scale leave such a step out.
  *
  * State in 32 bits (state_dtype F32): exp_avg holds m, exp_avg_sq v.
  * State in 8 bits (E4M3): exp_avg holds m and exp_avg_sq holds sqrt(v), each

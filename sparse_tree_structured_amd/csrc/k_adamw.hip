@@ -2,8 +2,10 @@
 // the gradient's norm over many tensors.
 //
 // Per element, with g already times *grad_scale:
-//   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
-//   p = p (1 - lr wd) - (lr / (1 - beta1^t)) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//   m = m beta1 + g (1 - beta1);   v = v beta2 + (g g) (1 - beta2)
+//   p = p decay - step (m / (sqrt(v) root + eps))
+// with decay = 1 - lr wd, step = lr / (1 - beta1^t) and root = 1 / sqrt(1 - beta2^t)
+// from the host, formed in 64 bits and rounded to 32.
 //
 // The products and sums are rounded one by one (no contraction), and division
 // and square root are IEEE, so the step gives the same bits as the formulas

@@ -1,10 +1,15 @@
-"""The host-side rules of the optimiser's launches, compiled from the
-library's own header with the host's compiler and run on the CPU."""
+"""The host-side rules of the optimiser, on the CPU: those of its launches,
+compiled from the library's own header with the host's compiler, and the
+formulas that the public header states."""
+import math
 import os
+import re
 import subprocess
 
+import numpy as np
 import pytest
 
+import train_oracle as O
 from sparse_tree_structured_amd import build as hipbuild
 
 PROGRAM = """
@@ -49,3 +54,36 @@ def test_a_large_launch_streams_whatever_its_size(program, kind):
     for blocks in ((1 << 20) - 1, 1 << 20, (1 << 20) + 1, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, 3 << 20, 1 << 23,
                    (1 << 24) - 1):
         assert program(blocks, *kind), blocks
+
+
+def test_the_headers_formulas_give_the_step_its_bits():
+    """The four lines that fff.h writes for an AdamW step, evaluated as they
+    stand in 32 bits, give the bits of the form the GPU's are compared with."""
+    with open(os.path.join(hipbuild.INCLUDE, "fff.h")) as f:
+        text = f.read()
+    text = text[text.index("AdamW (decoupled weight decay)"):]
+    found = re.findall(r"^ \*   (\w+) = (.*)$", text, re.M)
+    lines = [(k, v) for k, v in found[:4]]
+    consts = [(k, v) for k, v in found[4:7]]
+    assert [k for k, _ in lines] == ["g", "m", "v", "p"]
+    assert [k for k, _ in consts] == ["decay", "step_size", "root"]
+
+    kw = dict(lr=3e-3, beta1=0.9, beta2=0.99, eps=1e-8, wd=0.1, step=7)
+    names = {"lr": kw["lr"], "weight_decay": kw["wd"], "sqrt": math.sqrt,
+             **{k: kw[k] for k in ("beta1", "beta2", "step")}}
+    at = {k: np.float32(eval(v.replace("^", "**"), {}, names)) for k, v in consts}
+    at.update({k: np.float32(kw[k]) for k in ("beta1", "beta2", "eps")})
+    at.update(one_beta1=np.float32(1 - kw["beta1"]), one_beta2=np.float32(1 - kw["beta2"]), sqrt=np.sqrt)
+
+    rng = np.random.default_rng(5)
+    n = 100_000
+    p, grad, m = (rng.normal(size=n).astype(np.float32) for _ in range(3))
+    v = rng.random(n).astype(np.float32)
+    want = O.adamw(p, grad, m, v, gs=0.37, **kw)
+    at.update(p=p, grad=grad, m=m, v=v, grad_scale=np.float32(0.37))
+    for k, line in lines:
+        line = line.replace("(1 - beta1)", "one_beta1").replace("(1 - beta2)", "one_beta2")
+        at[k] = eval(line, {}, at)
+        assert at[k].dtype == np.float32
+    for k in "pmv":
+        assert np.array_equal(at[k], want[k]), k
