@@ -632,6 +632,7 @@ class _Torch:
         self.empty, self.stream = torch.empty, torch.cuda.stream
         self.device = getattr(torch._C, "_cuda_getDevice", None)
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 
 
 _lazy: Optional[_Torch] = None
@@ -661,6 +662,13 @@ def _empty(rt, shape, dtype, device, stream):
         return rt.empty(shape, dtype=dtype, device=device)
     with rt.stream(stream):
         return rt.empty(shape, dtype=dtype, device=device)
+
+
+def _capturing(rt, stream) -> bool:
+    if stream is None:
+        return rt.capturing()
+    with rt.stream(stream):
+        return rt.capturing()
 
 
 def _code(rt, dtype) -> int:
@@ -819,10 +827,14 @@ def rms_norm_backward(dy, z, weight, rstd, *, dresidual=None, weight_offset: flo
 
 class TensorTable:
     """The tensors of an optimiser, laid out for the library: made once by
-    adamw_table or grad_table, used at every step.  It keeps the tensors
-    alive; they are updated in place and must keep their storage (make
-    another table where a tensor is replaced).  One stream uses it at a time,
-    as for the tensors themselves."""
+    adamw_table or grad_table, used at every step.  It holds their addresses
+    and keeps the tensors alive; they are updated in place.  Where a tensor is
+    replaced, make another table: after zero_grad(set_to_none=True) the next
+    backward pass leaves other gradients in p.grad, and a step on this table
+    would read the old ones (zero them in place, or let the backward write
+    into them).  One stream uses it at a time, as for the tensors themselves.
+    A captured graph holds the tensors' addresses too and does not keep them
+    alive: keep the tensors, or the table, as long as the graph."""
 
     def __init__(self, entries, first, state_code, keep):
         self.entries = entries        # array of AdamwTensor
@@ -836,9 +848,8 @@ class TensorTable:
         if st != SUCCESS:
             raise FFFError(st, "fff_grad_norm_workspace_size")
         self.norm_workspace = n.value
-        # grad_norm's workspace on every stream that has used the table: kept as
-        # long as the table, for a captured graph keeps its address.
-        self._workspaces = {}
+        self._workspaces = {}  # grad_norm's workspace on every stream that has used the table
+        self._captured = []    # and those of its captured calls
 
 
 def _flat(t, n, dtypes, device, what):
@@ -1019,9 +1030,15 @@ def grad_norm(grads, *, max_norm: float = float("inf"), out=None, workspace=None
         pws = _tensor(workspace, (have,), rt.u8, table.first, "workspace")
     elif table.norm_workspace:
         have = table.norm_workspace
-        workspace = table._workspaces.get(handle)
-        if workspace is None:
-            workspace = table._workspaces[handle] = _empty(rt, (have,), rt.u8, table.device, stream)
+        if _capturing(rt, stream):
+            # From the capture's own memory, which the graph keeps: the table may
+            # go first, and a call beside a replay does not share it.
+            workspace = _empty(rt, (have,), rt.u8, table.device, stream)
+            table._captured.append(workspace)
+        else:
+            workspace = table._workspaces.get(handle)
+            if workspace is None:
+                workspace = table._workspaces[handle] = _empty(rt, (have,), rt.u8, table.device, stream)
         pws = workspace.data_ptr()
     st = (_lib or load_library()).fff_grad_norm(table.entries, table.count, max_norm, pout, pws, have, handle)
     if st != SUCCESS:

@@ -147,3 +147,31 @@ def test_backward_with_a_given_workspace(T, d):
         with pytest.raises(fff.FFFError) as e:
             fff.rms_norm_backward(dy, z, w, rstd, workspace=buf[:need - 1])
         assert e.value.status == fff.ERROR_WORKSPACE
+
+
+@pytest.mark.parametrize("before", [False, True])
+def test_a_captured_norm_outlives_its_table(before):
+    """A table used before the capture or not, then dropped: replays give the
+    eager result and touch no tensor that was made since."""
+    g = torch.randn(300_000, device=DEV)
+    table = fff.grad_table([g])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if before:
+        fff.grad_norm(table, stream=side)
+        side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = fff.grad_norm(table)
+    del table
+    with torch.cuda.stream(side):
+        other = [torch.full((64,), 7.0, device=DEV) for _ in range(100)]
+    other += [torch.full((64,), 7.0, device=DEV) for _ in range(100)]
+    print(f"[gpu] grad_norm captured, table dropped, before={before}", flush=True)
+    for _ in range(4):
+        g.normal_()
+        torch.cuda.synchronize()
+        want = fff.grad_norm([g])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and all(bool((o == 7.0).all()) for o in other)

@@ -171,3 +171,36 @@ def test_a_state_of_parameters_that_can_be_walked_once(on_cpu, bits):
     assert s is None if bits == 32 else [tuple(t.shape) for t in s] == [(5, 2), (1, 2)]
     grads = (torch.zeros_like(p) for p in module.parameters())
     assert fff.adamw_table(module.parameters(), grads, m, v, scales=s).count == 2
+
+
+def test_a_captured_norm_has_a_workspace_of_its_own(on_cpu, monkeypatch):
+    """Calls on a stream share the table's; a call that is captured gets
+    memory of the capture's, which lives as long as the graph, and the table
+    holds it besides for captures whose allocations no pool keeps."""
+    g = [torch.zeros(300_000)]
+    table = fff.grad_table(g)
+    assert table.norm_workspace > 0
+    used = []
+
+    class Stub:
+        def fff_grad_norm(self, entries, count, limit, out, workspace, size, stream):
+            used.append(workspace)
+            return fff.SUCCESS
+
+    class Capturing:
+        now = False
+
+        def __call__(self):
+            return self.now
+
+    capturing = Capturing()
+    monkeypatch.setattr(fff, "_lib", Stub())
+    monkeypatch.setattr(fff, "_here", lambda rt, t, stream: 0)
+    monkeypatch.setattr(fff._rt(), "capturing", capturing, raising=False)
+    for capturing.now in (False, False, True, True, False):
+        fff.grad_norm(table)
+    first, second, captured, again, last = used
+    assert first == second == last and len({first, captured, again}) == 3
+    del captured, again
+    held = {w.data_ptr() for w in list(table._workspaces.values()) + table._captured}
+    assert held == set(used)
