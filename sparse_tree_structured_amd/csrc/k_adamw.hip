@@ -84,10 +84,11 @@ struct Quad {
 // on the IBM RISC System/6000 processor", 1990): 36 cycles of a wavefront
 // each where the compiler's, which also serve operands near the ends of the
 // range, take 76 and 52; the 8-bit step is bound by them.  The root is the
-// IEEE one for v = 0 and every v in [2^-90, 2^60) (all compared); the
-// quotient for m = 0 and m in [2^-60, 2^60) over [2^-60, 2^90) (1e11 pairs
-// compared: 12288 divisors, the 4096 smallest and the 4096 largest mantissas
-// among them, with every mantissa of m).
+// IEEE one for v = 0 and every v in [2^-90, 2^60) (the tests compare all of
+// them).  The quotient is for m = 0 and m in [2^-60, 2^60) over [2^-60, 2^90):
+// no pair of 1e11 differed, every mantissa of m over 12288 divisors, the 4096
+// smallest and the 4096 largest mantissas among them.  That is a sample of
+// the divisors; the tests hold 48 of them.
 __device__ __forceinline__ float short_sqrt(float v) {
 #pragma clang fp contract(off)
   const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));  // (finite for v = 0)

@@ -175,3 +175,39 @@ def test_a_captured_norm_outlives_its_table(before):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and all(bool((o == 7.0).all()) for o in other)
+
+
+def quotients(m, v, eps):
+    """The step's m / (sqrt(v) + eps): betas of one half so late that their
+    corrections are 1, weights of zero, no gradient."""
+    n = len(m)
+    t = [torch.zeros(n, device=DEV), torch.zeros(n, device=DEV), dev(2 * m), dev(2 * v)]
+    fff.adamw_step(fff.adamw_table([t[0]], [t[1]], [t[2]], [t[3]]), lr=1.0, step=1000, beta1=0.5, beta2=0.5, eps=eps)
+    return -t[0].cpu().numpy()
+
+
+@pytest.mark.parametrize("first", range(-90, 60, 30))
+def test_every_root_of_the_short_form(first):
+    """All floats from 2^-90 to 2^60.  A root that is off by its last bit
+    shows in the quotient, whose own last bit is finer than the root's for one
+    of the two sizes of m."""
+    for low in range(first, first + 30, 2):
+        print(f"[gpu] adamw root of [2^{low}, 2^{low + 2})", flush=True)
+        v = np.arange((127 + low) << 23, (129 + low) << 23, dtype=np.uint32).view(np.float32)
+        d = np.sqrt(v) + np.float32(2.0 ** -60)
+        for m in (np.float32(1.0), np.float32(1.9999999)):
+            assert np.array_equal(quotients(np.full(len(v), m), v, 2.0 ** -60), m / d)
+
+
+@pytest.mark.parametrize("size", [-60, 0, 59])
+def test_the_quotient_of_every_mantissa(size):
+    """Every mantissa of m over the smallest and the largest mantissas of a
+    divisor and some between (v = 0: the divisor is eps)."""
+    rng = np.random.default_rng(23)
+    m = np.arange(127 << 23, 128 << 23, dtype=np.uint32).view(np.float32)
+    zero = np.zeros_like(m)
+    ends = [k for i in range(4) for k in (i, (1 << 23) - 1 - i)]
+    print(f"[gpu] adamw quotient over 2^{size}", flush=True)
+    for k in ends + list(rng.integers(0, 1 << 23, 8)):
+        d = np.float32((1 + int(k) * 2.0 ** -23) * 2.0 ** size)
+        assert np.array_equal(quotients(m, zero, float(d)), m / d), k
