@@ -896,25 +896,16 @@ def grad_table(grads) -> TensorTable:
     return TensorTable(entries, grads[0], None, grads)
 
 
-def _check_apart(entries, e4m3):
+def _check_apart(written, grads):
     """Refuses a table whose step would write some memory twice, or read a
     gradient where it writes: workgroups run in any order.  A gradient may be
-    a buffer of its own entry, whose elements a lane reads before it writes."""
-    size = {DTYPE_F32: 4, DTYPE_BF16: 2}
-    state = 1 if e4m3 else 4
-    written, grads = [], []
-    for i, e in enumerate(entries):
-        blocks = -(-e.n // ADAMW_BLOCK)
-        for name, at, n in (("params", e.param, e.n * size[e.param_dtype]), ("masters", e.master, e.n * 4),
-                            ("exp_avg", e.exp_avg, e.n * state), ("exp_avg_sq", e.exp_avg_sq, e.n * state),
-                            ("scales", e.scale, blocks * 8)):
-            if at and n:
-                written.append((at, at + n, i, name))
-        if e.n:
-            grads.append((e.grad, e.grad + e.n * size[e.grad_dtype], i))
+    a buffer of its own entry, whose elements a lane reads before it writes.
+    ``written``: (start, end, entry, name) of what is; ``grads``: (start, end,
+    entry)."""
     written.sort()
-    for (_, end, i, a), (start, _, j, b) in zip(written, written[1:]):
-        if start < end:
+    for before, w in zip(written, written[1:]):
+        if w[0] < before[1]:
+            (_, _, i, a), (_, _, j, b) = before, w
             raise ValueError(f"{a}[{i}] and {b}[{j}] share memory: every param, master, state and scale "
                              "must be its own")
     starts = [w[0] for w in written]
@@ -951,7 +942,7 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
     None where a param has none).  ``weight_decay`` and ``lr_scale``: one
     number, or one for each tensor.  No two tensors that a step writes may
     share memory."""
-    torch = _torch()
+    torch, rt = _torch(), _rt()
     params = list(params)
     n = len(params)
     if n == 0:
@@ -959,7 +950,7 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
     dev = params[0].device
     f32, both = (torch.float32,), (torch.float32, torch.bfloat16)
     lists = {"grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
-             "masters": masters, "scales": scales}
+             "masters": masters, "scales": scales}  # in the order of the loop below
     lists = {k: _tensors(v, n, k, torch) for k, v in lists.items()}
     decays, shares = _listed(weight_decay, n, "weight_decay"), _listed(lr_scale, n, "lr_scale")
     state = (lists["exp_avg"][0].dtype,)
@@ -967,24 +958,33 @@ def adamw_table(params, grads, exp_avg, exp_avg_sq, *, masters=None, scales=None
     if not e4m3 and state != f32:
         raise ValueError(f"exp_avg must be torch.float32 or torch.float8_e4m3fn, got {state[0]}")
     entries = (AdamwTensor * n)()
-    for i, (e, p) in enumerate(zip(entries, params)):
-        g, m, v, w, sc = (lists[k][i] for k in ("grads", "exp_avg", "exp_avg_sq", "masters", "scales"))
-        e.n = p.numel()
-        e.param = _flat(p, e.n, both, dev, f"params[{i}]")
-        e.grad = _flat(g, e.n, both, dev, f"grads[{i}]")
-        e.exp_avg = _flat(m, e.n, state, dev, f"exp_avg[{i}]")
-        e.exp_avg_sq = _flat(v, e.n, state, dev, f"exp_avg_sq[{i}]")
-        e.param_dtype, e.grad_dtype = _dtype_code(p), _dtype_code(g)
+    written, read, size = [], [], 1 if e4m3 else 4
+    for i, (e, p, g, m, v, w, sc) in enumerate(zip(entries, params, *lists.values())):
+        e.n = k = p.numel()
+        e.param = pp = _flat(p, k, both, dev, f"params[{i}]")
+        e.grad = pg = _flat(g, k, both, dev, f"grads[{i}]")
+        e.exp_avg = pm = _flat(m, k, state, dev, f"exp_avg[{i}]")
+        e.exp_avg_sq = pv = _flat(v, k, state, dev, f"exp_avg_sq[{i}]")
+        e.param_dtype, e.grad_dtype = code, grad_code = rt.codes[p.dtype], rt.codes[g.dtype]
+        if k:
+            written += ((pp, pp + (2 if code == DTYPE_BF16 else 4) * k, i, "params"),
+                        (pm, pm + size * k, i, "exp_avg"), (pv, pv + size * k, i, "exp_avg_sq"))
+            read.append((pg, pg + (2 if grad_code == DTYPE_BF16 else 4) * k, i))
         if w is not None:
             if p.dtype != torch.bfloat16:
                 raise ValueError(f"masters[{i}] is for a bf16 param, params[{i}] is {p.dtype}")
-            e.master = _flat(w, e.n, f32, dev, f"masters[{i}]")
+            e.master = pw = _flat(w, k, f32, dev, f"masters[{i}]")
+            if k:
+                written.append((pw, pw + 4 * k, i, "masters"))
         if e4m3 != (sc is not None):
             raise ValueError("scales go with exp_avg of torch.float8_e4m3fn, and only with it")
         if e4m3:
-            e.scale = _flat(sc, 2 * -(-e.n // ADAMW_BLOCK), f32, dev, f"scales[{i}]")
+            blocks = -(-k // ADAMW_BLOCK)
+            e.scale = ps = _flat(sc, 2 * blocks, f32, dev, f"scales[{i}]")
+            if k:
+                written.append((ps, ps + 8 * blocks, i, "scales"))
         e.lr_scale, e.weight_decay = float(shares[i]), float(decays[i])
-    _check_apart(entries, e4m3)
+    _check_apart(written, read)
     return TensorTable(entries, params[0], DTYPE_E4M3 if e4m3 else DTYPE_F32, (params, lists))
 
 
