@@ -75,7 +75,7 @@ struct Span {
 // Otherwise columns col + lo .. col + hi - 1 (nothing where lo = V).  An
 // access that would leave the row is moved back to end with it, so that every
 // load is a whole one inside the row and none waits for a short one (at
-// 8000 x 2703 in bf16 the forward takes 40.7 us instead of 53.6); what the
+// 8000 x 2703 in bf16 the forward takes 41.1 us instead of 53.6); what the
 // lane then has twice, below lo, counts for nothing and is not stored.
 template <int V>
 struct Span<V, true> {
