@@ -1006,6 +1006,8 @@ def adamw_step(table: TensorTable, *, lr: float, step: int, beta1: float = 0.9,
     handle = _here(rt, table.first, stream)
     config = AdamwConfig(lr, beta1, beta2, eps, step, table.state_code, seed is not None,
                          0 if seed is None else seed & 0xFFFFFFFFFFFFFFFF, ps)
+    if config.step != step:  # cut to its field
+        raise FFFError(ERROR_INVALID_VALUE, f"AdamW step {step}")
     st = (_lib or load_library()).fff_adamw_step(config, table.entries, table.count, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_adamw_step")

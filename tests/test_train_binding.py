@@ -204,3 +204,17 @@ def test_a_captured_norm_has_a_workspace_of_its_own(on_cpu, monkeypatch):
     del captured, again
     held = {w.data_ptr() for w in list(table._workspaces.values()) + table._captured}
     assert held == set(used)
+
+
+@pytest.mark.parametrize("step", [1 << 63, (1 << 64) + 1, -(1 << 64) + 1])
+def test_a_step_beyond_its_field_is_refused(on_cpu, monkeypatch, step):
+    """In 64 bits the last two would be the first step."""
+    t = table(tensors())
+    stub = Library()
+    monkeypatch.setattr(fff, "_lib", stub)
+    monkeypatch.setattr(fff, "_here", lambda rt, t, stream: 0)
+    with pytest.raises(fff.FFFError) as e:
+        fff.adamw_step(t, lr=1e-3, step=step)
+    assert e.value.status == fff.ERROR_INVALID_VALUE and not stub.shapes
+    fff.adamw_step(t, lr=1e-3, step=(1 << 63) - 1)
+    assert stub.shapes.pop().step == (1 << 63) - 1
