@@ -431,7 +431,8 @@ fff_status_t fff_forward_static(const fff_shape_t *shape, const fff_plan_t *plan
  * short) scale = max(largest |y| * (1/448), 2^-126) and the stored value is
  * y * (1/scale) to nearest (both reciprocals rounded to 32 bits).  A NaN in
  * a group makes its scale NaN; a group whose largest size is infinite has
- * scale infinity.
+ * scale infinity.  The 8-bit y is for a product of the caller's own: the
+ * layer's entry points take F32 and BF16.
  */
 typedef struct fff_norm_shape {
     int64_t T;             /* rows, 0 <= T < 2^31 */
