@@ -72,7 +72,7 @@ typedef enum fff_dtype {
     FFF_DTYPE_F32 = 0,
     FFF_DTYPE_BF16 = 1,
     FFF_DTYPE_E4M3 = 2 /* 8-bit float (OCP: 4 exponent, 3 mantissa bits): the norm's
-                          output and the optimiser's states only */
+                          output, the optimiser's states and checkpoints only */
 } fff_dtype_t;
 
 typedef enum fff_status {
@@ -568,6 +568,151 @@ fff_status_t fff_grad_norm_workspace_size(const fff_adamw_tensor_t *tensors, int
 fff_status_t fff_grad_norm(const fff_adamw_tensor_t *tensors, int64_t count, double max_norm,
                            float *out, void *workspace, size_t workspace_bytes,
                            hipStream_t stream);
+
+/*
+ * Dense feed-forward block
+ * ------------------------
+ * The dense layer that an FFF layer takes the place of: a matrix product with
+ * bias, activation and residual in its epilogue, the gated pair of
+ * projections, the backward passes of both, and activations kept for them in
+ * 8 bits.  The rules above hold: dense row-major device tensors, caller-owned
+ * workspaces, no state, validation before any HIP call.  Pointers need an
+ * element's alignment only (workspaces 256 bytes); bf16 tensors of 16-byte
+ * alignment whose widths are multiples of 8 take the fastest kernels.
+ *
+ * Weights are [inputs, outputs], as W_out:
+ *   linear   a = x . W + bias          y = act(a) + residual
+ *   gated    g = x . W_gate, u = x . W_up          h = act(g) * u
+ * act is one of
+ *   NONE a     GELU a q(2 sqrt(2/pi) (a + 0.044715 a^3)) (the tanh form)
+ *   SILU a q(a)     RELU max(a, 0)          with q(z) = 1 / (1 + exp(-z))
+ * Sums and activations are in 32 bits and outputs rounded once; bf16 products
+ * are exact, float32 ones rounded to 32 bits.  a, or g and u, can be kept for
+ * the backward pass as they are before the activation, in the layer's type
+ * or in 8 bits.
+ *
+ * 8 bits (FFF_DTYPE_E4M3) are those of fff_rms_norm: a float32 scale for every
+ * row (group 0) or every `group` columns of one (32, 64 or 128; the last group
+ * may be short), scale = max(largest size * (1/448), 2^-126), code = value *
+ * (1/scale) to nearest; the value that is read back is code * scale.  So the
+ * norm's 8-bit output is a checkpoint of it.
+ *
+ * Backward, with a (or g, u) and x as they were kept:
+ *   linear   da = dy * act'(a)
+ *            dx = da . W^T     dW = x^T . da     dbias = sum over rows of da
+ *   gated    dg = dh * u * act'(g),  du = dh * act(g)
+ *            dx = dg . W_gate^T + du . W_up^T
+ *            dW_gate = x^T . dg,  dW_up = x^T . du
+ *            h = act(g) * u, made again for the product that follows it
+ * act' of RELU is 0 at 0.  The products' operands are of the layer's type: in
+ * a bf16 layer da (where there is an activation), dg, du and an x kept in 8
+ * bits are rounded to bf16 once, which moves a gradient by about 2^-9 of its
+ * size; sums are in 32 bits.  dy itself is dresidual.
+ */
+#define FFF_DENSE_MAX_WIDTH (1 << 20)
+
+typedef enum fff_act {
+    FFF_ACT_NONE = 0,
+    FFF_ACT_GELU = 1,
+    FFF_ACT_SILU = 2,
+    FFF_ACT_RELU = 3
+} fff_act_t;
+
+typedef struct fff_dense_shape {
+    int64_t T;           /* rows, 0 <= T < 2^31 */
+    int32_t K, N;        /* inputs and outputs (of each of a gated pair), 1 up to
+                            FFF_DENSE_MAX_WIDTH; every tensor below 2^40 elements.
+                            FFF_ERROR_NOT_SUPPORTED beyond either, or where an
+                            output has 2^22 tiles of 128 x 128 or more */
+    int32_t dtype;       /* F32 or BF16: x, weights, bias, dy, dx, dh, h */
+    int32_t out_dtype;   /* linear: of residual and y, `dtype` or F32; gated: `dtype`
+                            (the backward passes ignore it) */
+    int32_t act;         /* fff_act_t */
+    int32_t save_dtype;  /* `dtype` or E4M3: a, g and u as they are kept */
+    int32_t save_group;  /* their columns per scale with E4M3 (32, 64 or 128, or 0 in
+                            the backward passes), else 0 */
+    int32_t x_dtype;     /* backward: x as it is kept, `dtype` or E4M3 */
+    int32_t x_group;     /* its columns per scale with E4M3 (0, 32, 64 or 128), else 0 */
+    int32_t grad_dtype;  /* backward: of dW, `dtype` or F32 */
+} fff_dense_shape_t;
+
+/*
+ *   x         [T,K] dtype             W          [K,N] dtype
+ *   bias      [N] dtype, or NULL      residual   [T,N] out_dtype, or NULL
+ *   y         [T,N] out_dtype
+ *   pre       [T,N] save_dtype: a, or NULL
+ *   pre_scale [T, ceil(N / save_group)] float32; E4M3 only
+ * y may be the buffer of the residual; no other overlap is allowed.  T = 0 is
+ * a no-op.  Results are the same on every call (no atomics).
+ */
+fff_status_t fff_linear_workspace_size(const fff_dense_shape_t *shape, size_t *bytes);
+fff_status_t fff_linear(const fff_dense_shape_t *shape, const void *x, const void *W,
+                        const void *bias, const void *residual, void *y, void *pre,
+                        float *pre_scale, void *workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/*
+ *   dy     [T,N] dtype
+ *   x      [T,K] x_dtype, with x_scale [T, groups] float32 for E4M3 (dW only)
+ *   W      [K,N] dtype (dx only)
+ *   pre    [T,N] save_dtype, with pre_scale for E4M3 (act other than NONE only)
+ *   dx     [T,K] dtype, or NULL        dW     [K,N] grad_dtype, or NULL
+ *   dbias  [N] float32, or NULL
+ * Every output is overwritten and may overlap nothing else.  T = 0 gives dW
+ * and dbias 0.  Sums over rows are in a fixed order.  The workspace size
+ * depends on the shape alone, whatever outputs are asked for.
+ */
+fff_status_t fff_linear_backward_workspace_size(const fff_dense_shape_t *shape, size_t *bytes);
+fff_status_t fff_linear_backward(const fff_dense_shape_t *shape, const void *dy, const void *x,
+                                 const float *x_scale, const void *W, const void *pre,
+                                 const float *pre_scale, void *dx, void *dW, float *dbias,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ *   x         [T,K] dtype             W_gate, W_up  [K,N] dtype
+ *   h         [T,N] dtype
+ *   gate, up  [T,N] save_dtype: g and u, each or NULL, with gate_scale and
+ *             up_scale [T, ceil(N / save_group)] float32 for E4M3
+ * Both projections, the activation and the product are one kernel (and a sum
+ * of its parts where K is cut for small T).  No overlap is allowed.  T = 0 is
+ * a no-op.
+ */
+fff_status_t fff_gated_workspace_size(const fff_dense_shape_t *shape, size_t *bytes);
+fff_status_t fff_gated(const fff_dense_shape_t *shape, const void *x, const void *W_gate,
+                       const void *W_up, void *h, void *gate, float *gate_scale, void *up,
+                       float *up_scale, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ *   dh                [T,N] dtype
+ *   x, x_scale        as for fff_linear_backward (dW_gate and dW_up only)
+ *   W_gate, W_up      [K,N] dtype (dx only)
+ *   gate, up          [T,N] save_dtype, with their scales for E4M3
+ *   dx                [T,K] dtype, or NULL
+ *   dW_gate, dW_up    [K,N] grad_dtype, both or neither
+ *   h                 [T,N] dtype, or NULL
+ * Every output is overwritten and may overlap nothing else.  T = 0 gives the
+ * weights' gradients 0.
+ */
+fff_status_t fff_gated_backward_workspace_size(const fff_dense_shape_t *shape, size_t *bytes);
+fff_status_t fff_gated_backward(const fff_dense_shape_t *shape, const void *dh, const void *x,
+                                const float *x_scale, const void *W_gate, const void *W_up,
+                                const void *gate, const float *gate_scale, const void *up,
+                                const float *up_scale, void *dx, void *dW_gate, void *dW_up,
+                                void *h, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/*
+ * Rows x [T,d] of F32 or BF16 into 8 bits (codes [T,d], scale [T, groups]) and
+ * back.  A NaN in a group makes its scale NaN; a group whose largest size is
+ * infinite has scale infinity, and reads back as NaN.  No overlap is allowed.
+ * 1 <= d <= FFF_DENSE_MAX_WIDTH; T = 0 is a no-op.
+ */
+fff_status_t fff_checkpoint_save(int64_t T, int32_t d, int32_t dtype, int32_t group, const void *x,
+                                 void *codes, float *scale, hipStream_t stream);
+fff_status_t fff_checkpoint_load(int64_t T, int32_t d, int32_t dtype, int32_t group,
+                                 const void *codes, const float *scale, void *x,
+                                 hipStream_t stream);
 
 /* Static, human-readable text for a status code. */
 const char *fff_status_string(fff_status_t status);

@@ -39,7 +39,10 @@ PLAN_TEST_DECODE_NO_PUBLISH = 1
 VARIANT_FFF = 0
 VARIANT_POST = 1
 VARIANTS = {"fff": VARIANT_FFF, "post": VARIANT_POST}
+# fff_act_t
+ACTS = {"none": 0, "gelu": 1, "silu": 2, "relu": 3}
 MAX_DEPTH = 20
+DENSE_MAX_WIDTH = 1 << 20  # FFF_DENSE_MAX_WIDTH
 
 
 class Shape(ctypes.Structure):
@@ -93,6 +96,15 @@ class AdamwConfig(ctypes.Structure):
                 ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p)]
 
 
+class DenseShape(ctypes.Structure):
+    """fff_dense_shape_t."""
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("save_dtype", ctypes.c_int32), ("save_group", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("x_group", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32)]
+
+
 class FFFError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -106,7 +118,11 @@ EXPORTS = ("fff_plan_default", "fff_plan_resolve", "fff_workspace_size", "fff_fo
            "fff_backward_workspace_size", "fff_backward", "fff_forward_static",
            "fff_backward_pruned_workspace_size", "fff_backward_pruned",
            "fff_rms_norm", "fff_rms_norm_backward_workspace_size", "fff_rms_norm_backward",
-           "fff_adamw_step", "fff_grad_norm_workspace_size", "fff_grad_norm")
+           "fff_adamw_step", "fff_grad_norm_workspace_size", "fff_grad_norm",
+           "fff_linear_workspace_size", "fff_linear", "fff_linear_backward_workspace_size",
+           "fff_linear_backward", "fff_gated_workspace_size", "fff_gated",
+           "fff_gated_backward_workspace_size", "fff_gated_backward",
+           "fff_checkpoint_save", "fff_checkpoint_load")
 ADAMW_BLOCK = 128  # FFF_ADAMW_BLOCK: elements per scale of an 8-bit state
 STATIC_SCRATCH_BYTES = 32 << 20  # FFF_STATIC_SCRATCH_BYTES
 
@@ -153,6 +169,16 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.fff_adamw_step.argtypes = [ctypes.POINTER(AdamwConfig), TP, ctypes.c_int64, vp]
     lib.fff_grad_norm_workspace_size.argtypes = [TP, ctypes.c_int64, ctypes.POINTER(sz)]
     lib.fff_grad_norm.argtypes = [TP, ctypes.c_int64, ctypes.c_double, vp, vp, sz, vp]
+    DP, i32, i64 = ctypes.POINTER(DenseShape), ctypes.c_int32, ctypes.c_int64
+    for name in ("fff_linear", "fff_gated"):
+        getattr(lib, name + "_workspace_size").argtypes = [DP, ctypes.POINTER(sz)]
+        getattr(lib, name + "_backward_workspace_size").argtypes = [DP, ctypes.POINTER(sz)]
+    lib.fff_linear.argtypes = [DP] + [vp] * 8 + [sz, vp]
+    lib.fff_linear_backward.argtypes = [DP] + [vp] * 10 + [sz, vp]
+    lib.fff_gated.argtypes = [DP] + [vp] * 9 + [sz, vp]
+    lib.fff_gated_backward.argtypes = [DP] + [vp] * 14 + [sz, vp]
+    lib.fff_checkpoint_save.argtypes = [i64, i32, i32, i32, vp, vp, vp, vp]
+    lib.fff_checkpoint_load.argtypes = [i64, i32, i32, i32, vp, vp, vp, vp]
     lib.fff_status_string.argtypes = [ctypes.c_int]
     lib.fff_status_string.restype = ctypes.c_char_p
     lib.fff_algo_name.argtypes = [ctypes.c_int32]
@@ -163,7 +189,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "fff_forward_pruned", "fff_backward_workspace_size", "fff_backward",
                  "fff_forward_static", "fff_rms_norm", "fff_rms_norm_backward_workspace_size",
                  "fff_rms_norm_backward", "fff_adamw_step", "fff_grad_norm_workspace_size",
-                 "fff_grad_norm"):
+                 "fff_grad_norm", "fff_linear_workspace_size", "fff_linear",
+                 "fff_linear_backward_workspace_size", "fff_linear_backward",
+                 "fff_gated_workspace_size", "fff_gated", "fff_gated_backward_workspace_size",
+                 "fff_gated_backward", "fff_checkpoint_save", "fff_checkpoint_load"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -1045,4 +1074,314 @@ def grad_norm(grads, *, max_norm: float = float("inf"), out=None, workspace=None
     st = (_lib or load_library()).fff_grad_norm(table.entries, table.count, max_norm, pout, pws, have, handle)
     if st != SUCCESS:
         raise FFFError(st, "fff_grad_norm")
+    return out
+
+
+# ---- dense feed-forward block ----
+
+class Checkpoint(NamedTuple):
+    """Rows kept in 8 bits: what checkpoint() makes, linear() and gated() save
+    and their backward passes read.  rms_norm's 8-bit output is one too:
+    Checkpoint(o.y, o.scale, group)."""
+    codes: object  # [T,d] float8_e4m3fn
+    scale: object  # [T, groups] float32 ([T, 1] with group 0)
+    group: int     # columns per scale, 0: the row
+
+
+class Linear(NamedTuple):
+    y: object    # [T,N]
+    pre: object  # [T,N] before the activation: a tensor, a Checkpoint, or None
+
+
+class LinearGrad(NamedTuple):
+    dx: object     # [T,K], or None where not asked for (so the others)
+    dW: object     # [K,N]
+    dbias: object  # [N] float32
+
+
+class Gated(NamedTuple):
+    h: object     # [T,F] act(x . W_gate) * (x . W_up)
+    gate: object  # [T,F] x . W_gate: a tensor, a Checkpoint, or None
+    up: object    # [T,F] x . W_up
+
+
+class GatedGrad(NamedTuple):
+    dx: object      # [T,d], or None where not asked for (so the others)
+    dW_gate: object  # [d,F]
+    dW_up: object   # [d,F]
+    h: object       # [T,F] made again from gate and up
+
+
+@functools.lru_cache(maxsize=256)
+def _dense(name, T, K, N, dtype, out_dtype, act, save_dtype, save_group, x_dtype, x_group,
+           grad_dtype):
+    """The descriptor of these sizes, which the library only reads, and the
+    workspace bytes of the entry point `name` on them."""
+    s = DenseShape(T, K, N, dtype, out_dtype, act, save_dtype, save_group, x_dtype, x_group,
+                   grad_dtype)
+    # ctypes cuts a number that its field cannot hold
+    if s.K != K or s.N != N:
+        raise FFFError(ERROR_NOT_SUPPORTED, f"{name} of {K} inputs and {N} outputs")
+    if s.save_group != save_group or s.x_group != x_group:
+        raise FFFError(ERROR_INVALID_VALUE, f"{name} with groups {save_group}, {x_group}")
+    n = ctypes.c_size_t()
+    st = getattr(load_library(), name + "_workspace_size")(ctypes.byref(s), ctypes.byref(n))
+    if st != SUCCESS:
+        raise FFFError(st, name)
+    return s, n.value
+
+
+def _act_code(act) -> int:
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return code
+
+
+def _matrix(t, what):
+    """The shape of a contiguous matrix."""
+    if len(t.shape) != 2:
+        raise ValueError(f"{what} must have 2 dimensions, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.shape
+
+
+def _scales(T, d, group):
+    return (T, -(-d // group) if group > 0 else 1)
+
+
+def _kept(rt, t, shape, ty, like, what):
+    """Pointers, dtype code and group of a tensor or a Checkpoint."""
+    if isinstance(t, Checkpoint):
+        if not isinstance(t.group, int) or t.group not in (0, 32, 64, 128):
+            raise ValueError(f"{what} must have group 0, 32, 64 or 128, got {t.group}")
+        scale = _tensor(t.scale, _scales(*shape, t.group), rt.f32, like, f"{what}'s scale")
+        return _tensor(t.codes, shape, rt.f8, like, f"{what}'s codes"), scale, DTYPE_E4M3, t.group
+    return _tensor(t, shape, ty, like, what), 0, _code(rt, ty), 0
+
+
+def _workspace(rt, workspace, need, like, stream):
+    """A workspace tensor, its pointer and its bytes."""
+    if workspace is not None:
+        have = workspace.numel()
+        return workspace, _tensor(workspace, (have,), rt.u8, like, "workspace"), have
+    if not need:
+        return None, 0, 0
+    workspace = _empty(rt, (need,), rt.u8, like.device, stream)
+    return workspace, workspace.data_ptr(), need
+
+
+def _output(rt, t, shape, dtype, like, what, stream):
+    """An output tensor, made where there is none, and its pointer."""
+    if t is not None:
+        return t, _tensor(t, shape, dtype, like, what)
+    t = _empty(rt, shape, dtype, like.device, stream)
+    return t, t.data_ptr()
+
+
+def _save_kind(rt, save, group, ty, code):
+    """Dtype code and group of what is saved."""
+    if save not in (None, "same", "e4m3"):
+        raise ValueError(f'save must be None, "same" or "e4m3", got {save!r}')
+    return (DTYPE_E4M3, group) if save == "e4m3" else (code, 0)
+
+
+def _saved(rt, save, group, shape, ty, like, stream):
+    """A tensor or Checkpoint for saved sums, and its pointers."""
+    if save is None:
+        return None, 0, 0
+    t = _empty(rt, shape, rt.f8 if save == "e4m3" else ty, like.device, stream)
+    if save == "same":
+        return t, t.data_ptr(), 0
+    scale = _empty(rt, _scales(*shape, group), rt.f32, like.device, stream)
+    return Checkpoint(t, scale, group), t.data_ptr(), scale.data_ptr()
+
+
+def linear(x, W, bias=None, *, residual=None, act: str = "none", out_dtype=None,
+           save: Optional[str] = None, group: int = 128, y=None, workspace=None,
+           stream=None) -> Linear:
+    """fff_linear: y = act(x . W + bias) + residual, x [T,K], W [K,N].
+
+    ``act``: "none", "gelu" (tanh form), "silu" or "relu".  y and the residual
+    are of the layer's dtype, or float32 beside a bf16 layer (``out_dtype``,
+    else the residual's or y's dtype); ``y`` may be ``residual`` itself.
+    ``save`` keeps x . W + bias for linear_backward: "same" in the layer's
+    dtype, "e4m3" in 8 bits with a scale per ``group`` = 32, 64 or 128 columns."""
+    rt = _rt()
+    T, K = _matrix(x, "x [T,K]")
+    K2, N = _matrix(W, "W [K,N]")
+    ty = x.dtype
+    code = _code(rt, ty)
+    pw = _tensor(W, (K, N), ty, x, "W [K,N]")
+    pb = _tensor(bias, (N,), ty, x, "bias [N]") if bias is not None else 0
+    if out_dtype is None:
+        out_dtype = residual.dtype if residual is not None else y.dtype if y is not None else ty
+    pr = _tensor(residual, (T, N), out_dtype, x, "residual") if residual is not None else 0
+    save_code, save_group = _save_kind(rt, save, group, ty, code)
+    sizes, need = _dense("fff_linear", T, K, N, code, _code(rt, out_dtype), _act_code(act),
+                         save_code, save_group, code, 0, code)
+    handle = _here(rt, x, stream)
+    y, py = _output(rt, y, (T, N), out_dtype, x, "y", stream)
+    pre, pp, ps = _saved(rt, save, group, (T, N), ty, x, stream)
+    workspace, pws, have = _workspace(rt, workspace, need, x, stream)
+    st = (_lib or load_library()).fff_linear(sizes, x.data_ptr(), pw, pb, pr, py, pp, ps, pws, have,
+                                             handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_linear")
+    return Linear(y, pre)
+
+
+def linear_backward(dy, x, W, *, act: str = "none", pre=None, want_dx: bool = True,
+                    want_dW: bool = True, want_dbias: bool = False, grad_dtype=None, dx=None,
+                    dW=None, dbias=None, workspace=None, stream=None) -> LinearGrad:
+    """fff_linear_backward: the gradients of linear's inputs from dy [T,N]
+    (which itself is the residual's).  ``x`` [T,K] is a tensor or a Checkpoint
+    (None where dW is not wanted), ``pre`` what linear saved (a tensor or a
+    Checkpoint; needed with an activation).  dW is float32, or of
+    ``grad_dtype``; dbias is float32.  Outputs that are passed are filled."""
+    rt = _rt()
+    T, N = _matrix(dy, "dy [T,N]")
+    K, N2 = _matrix(W, "W [K,N]")
+    ty = dy.dtype
+    code, act_code = _code(rt, ty), _act_code(act)
+    pw = _tensor(W, (K, N), ty, dy, "W [K,N]")
+    px = pxs = pp = pps = pdx = pdw = pdb = x_group = save_group = 0
+    x_code = save_code = code
+    want_dx, want_dW = want_dx or dx is not None, want_dW or dW is not None
+    if want_dW:
+        if x is None:
+            raise ValueError("dW needs x")
+        px, pxs, x_code, x_group = _kept(rt, x, (T, K), ty, dy, "x [T,K]")
+    if act_code:
+        if pre is None:
+            raise ValueError(f"act {act!r} needs what linear saved")
+        pp, pps, save_code, save_group = _kept(rt, pre, (T, N), ty, dy, "pre [T,N]")
+    grad_dtype = grad_dtype or (dW.dtype if dW is not None else rt.f32)
+    sizes, need = _dense("fff_linear_backward", T, K, N, code, code, act_code, save_code, save_group,
+                         x_code, x_group, _code(rt, grad_dtype))
+    handle = _here(rt, dy, stream)
+    if want_dx:
+        dx, pdx = _output(rt, dx, (T, K), ty, dy, "dx", stream)
+    if want_dW:
+        dW, pdw = _output(rt, dW, (K, N), grad_dtype, dy, "dW", stream)
+    if want_dbias or dbias is not None:
+        dbias, pdb = _output(rt, dbias, (N,), rt.f32, dy, "dbias", stream)
+    workspace, pws, have = _workspace(rt, workspace, need, dy, stream)
+    st = (_lib or load_library()).fff_linear_backward(sizes, dy.data_ptr(), px, pxs, pw, pp, pps, pdx,
+                                                      pdw, pdb, pws, have, handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_linear_backward")
+    return LinearGrad(dx, dW, dbias)
+
+
+def gated(x, W_gate, W_up, *, act: str = "silu", save: Optional[str] = None, group: int = 128, h=None,
+          workspace=None, stream=None) -> Gated:
+    """fff_gated: h = act(x . W_gate) * (x . W_up), x [T,d], weights [d,F], in
+    one kernel.  ``save`` keeps both projections for gated_backward, as
+    linear's does."""
+    rt = _rt()
+    T, d = _matrix(x, "x [T,d]")
+    d2, F = _matrix(W_gate, "W_gate [d,F]")
+    ty = x.dtype
+    code = _code(rt, ty)
+    pg = _tensor(W_gate, (d, F), ty, x, "W_gate [d,F]")
+    pu = _tensor(W_up, (d, F), ty, x, "W_up [d,F]")
+    save_code, save_group = _save_kind(rt, save, group, ty, code)
+    sizes, need = _dense("fff_gated", T, d, F, code, code, _act_code(act), save_code, save_group, code,
+                         0, code)
+    handle = _here(rt, x, stream)
+    h, ph = _output(rt, h, (T, F), ty, x, "h", stream)
+    gate, p0, s0 = _saved(rt, save, group, (T, F), ty, x, stream)
+    up, p1, s1 = _saved(rt, save, group, (T, F), ty, x, stream)
+    workspace, pws, have = _workspace(rt, workspace, need, x, stream)
+    st = (_lib or load_library()).fff_gated(sizes, x.data_ptr(), pg, pu, ph, p0, s0, p1, s1, pws, have,
+                                            handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_gated")
+    return Gated(h, gate, up)
+
+
+def gated_backward(dh, x, W_gate, W_up, gate, up, *, act: str = "silu", want_dx: bool = True,
+                   want_dW: bool = True, want_h: bool = False, grad_dtype=None, dx=None, dW_gate=None,
+                   dW_up=None, h=None, workspace=None, stream=None) -> GatedGrad:
+    """fff_gated_backward: the gradients of gated's inputs from dh [T,F].
+    ``gate`` and ``up`` are what gated saved (tensors, or Checkpoints of one
+    group), ``x`` [T,d] a tensor or a Checkpoint (None where the weights'
+    gradients are not wanted).  ``want_h``: h made again from gate and up, for
+    the product that follows.  The weights' gradients are float32, or of
+    ``grad_dtype``.  Outputs that are passed are filled."""
+    rt = _rt()
+    T, F = _matrix(dh, "dh [T,F]")
+    d, F2 = _matrix(W_gate, "W_gate [d,F]")
+    ty = dh.dtype
+    code = _code(rt, ty)
+    pg = _tensor(W_gate, (d, F), ty, dh, "W_gate [d,F]")
+    pu = _tensor(W_up, (d, F), ty, dh, "W_up [d,F]")
+    p0, s0, save_code, save_group = _kept(rt, gate, (T, F), ty, dh, "gate [T,F]")
+    p1, s1, up_code, up_group = _kept(rt, up, (T, F), ty, dh, "up [T,F]")
+    if (up_code, up_group) != (save_code, save_group):
+        raise ValueError("gate and up must be kept alike")
+    px = pxs = pdx = pdg = pdu = ph = x_group = 0
+    x_code = code
+    if (dW_gate is None) != (dW_up is None):
+        raise ValueError("dW_gate and dW_up go together")
+    want_dx, want_dW = want_dx or dx is not None, want_dW or dW_gate is not None
+    if want_dW:
+        if x is None:
+            raise ValueError("the weights' gradients need x")
+        px, pxs, x_code, x_group = _kept(rt, x, (T, d), ty, dh, "x [T,d]")
+    grad_dtype = grad_dtype or (dW_gate.dtype if dW_gate is not None else rt.f32)
+    sizes, need = _dense("fff_gated_backward", T, d, F, code, code, _act_code(act), save_code,
+                         save_group, x_code, x_group, _code(rt, grad_dtype))
+    handle = _here(rt, dh, stream)
+    if want_dx:
+        dx, pdx = _output(rt, dx, (T, d), ty, dh, "dx", stream)
+    if want_dW:
+        dW_gate, pdg = _output(rt, dW_gate, (d, F), grad_dtype, dh, "dW_gate", stream)
+        dW_up, pdu = _output(rt, dW_up, (d, F), grad_dtype, dh, "dW_up", stream)
+    if want_h or h is not None:
+        h, ph = _output(rt, h, (T, F), ty, dh, "h", stream)
+    workspace, pws, have = _workspace(rt, workspace, need, dh, stream)
+    st = (_lib or load_library()).fff_gated_backward(sizes, dh.data_ptr(), px, pxs, pg, pu, p0, s0, p1,
+                                                     s1, pdx, pdg, pdu, ph, pws, have, handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_gated_backward")
+    return GatedGrad(dx, dW_gate, dW_up, h)
+
+
+def checkpoint(x, group: int = 128, *, codes=None, scale=None, stream=None) -> Checkpoint:
+    """fff_checkpoint_save: rows x [T,d] in 8 bits with a float32 scale for
+    every ``group`` = 32, 64 or 128 columns, or (0) for the row."""
+    rt = _rt()
+    T, d = _matrix(x, "x [T,d]")
+    code = _code(rt, x.dtype)
+    if group not in (0, 32, 64, 128):
+        raise FFFError(ERROR_INVALID_VALUE, f"checkpoint with group {group}")
+    if d > DENSE_MAX_WIDTH:
+        raise FFFError(ERROR_NOT_SUPPORTED, f"checkpoint of rows of {d} columns")
+    handle = _here(rt, x, stream)
+    codes, pc = _output(rt, codes, (T, d), rt.f8, x, "codes", stream)
+    scale, ps = _output(rt, scale, _scales(T, d, group), rt.f32, x, "scale", stream)
+    st = (_lib or load_library()).fff_checkpoint_save(T, d, code, group, x.data_ptr(), pc, ps, handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_checkpoint_save")
+    return Checkpoint(codes, scale, group)
+
+
+def restore(kept: Checkpoint, dtype=None, *, out=None, stream=None):
+    """fff_checkpoint_load: the rows that a Checkpoint stands for, in ``dtype``
+    (bf16 by default, or float32)."""
+    rt = _rt()
+    T, d = _matrix(kept.codes, "codes [T,d]")
+    if d > DENSE_MAX_WIDTH:
+        raise FFFError(ERROR_NOT_SUPPORTED, f"checkpoint of rows of {d} columns")
+    pc, ps, _, group = _kept(rt, kept, (T, d), rt.f8, kept.codes, "kept")
+    dtype = dtype or (out.dtype if out is not None else rt.bf16)
+    code = _code(rt, dtype)
+    handle = _here(rt, kept.codes, stream)
+    out, po = _output(rt, out, (T, d), dtype, kept.codes, "out", stream)
+    st = (_lib or load_library()).fff_checkpoint_load(T, d, code, group, pc, ps, po, handle)
+    if st != SUCCESS:
+        raise FFFError(st, "fff_checkpoint_load")
     return out

@@ -1,0 +1,258 @@
+// Elementwise part of the dense block's backward passes, column sums, and
+// activation checkpoints in 8 bits.  All are bound by HBM.
+#include <type_traits>
+
+#include "dense.hpp"
+#include "launch_dense.hpp"
+
+namespace fff {
+namespace {
+
+// Columns a lane has: one 16-byte access of the layer's type.
+template <typename E> constexpr int kLaneCols = 16 / int(sizeof(E));
+
+__host__ __device__ constexpr int there(int64_t left, int most) {
+  return left < 0 ? 0 : left < most ? static_cast<int>(left) : most;
+}
+
+// A value kept for the backward pass, in the layer's type or in 8 bits.
+template <typename E, int V>
+__device__ __forceinline__ void load_saved(float (&v)[V], const void* save, const float* scale,
+                                           int group, size_t row, int col, int N, int n) {
+  if (scale) {
+    Pack<uint8_t, V> q;
+    q.load(static_cast<const uint8_t*>(save) + row * N + col, n);
+    unpack_e4m3(q, v);
+    if (n <= 0) return;
+    // V divides the group, and col is a multiple of V: one scale a lane
+    const float s = scale[row * ((N + group - 1) / group) + col / group];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] *= s;
+  } else {
+    Pack<E, V> q;
+    q.load(static_cast<const E*>(save) + row * N + col, n);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = q.get(i);
+  }
+}
+
+// Rows of one workgroup: four wavefronts take every fourth.
+constexpr int kStripRows = 64;
+constexpr int64_t kMaxStrips = 1024;  // of rows, where columns are summed
+
+// da = dy act'(pre); of the gated pair dgate = dh up act'(gate) and dup = dh
+// act(gate), h = act(gate) up.  A workgroup has 64 lanes of columns and a
+// strip of rows; column sums are added over its rows in order, then over its
+// wavefronts, and one partial sum a strip is left for sum_strips_kernel.
+template <typename E, bool GATED>
+__global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int col_blocks,
+                                                           int64_t strips) {
+  constexpr int V = kLaneCols<E>;
+  __shared__ float sums[GATED ? 1 : 4][GATED ? 1 : kWave * V];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = threadIdx.x / kWave;
+  const int64_t strip = blockIdx.x / col_blocks;
+  const int col = (blockIdx.x % col_blocks * kWave + lane) * V;
+  const int n = there(a.N - col, V);
+  float total[V] = {};
+  for (int64_t r0 = strip * kStripRows; r0 < a.T; r0 += strips * kStripRows) {
+    const int64_t end = r0 + kStripRows < a.T ? r0 + kStripRows : a.T;
+    for (int64_t t = r0 + wave; t < end; t += 4) {
+      const size_t row = static_cast<size_t>(t);
+      Pack<E, V> dy;
+      dy.load(static_cast<const E*>(a.dy) + row * a.N + col, n);
+      float pre[V], up[V], da[V];
+      if (a.save[0]) load_saved<E>(pre, a.save[0], a.scale[0], a.group, row, col, a.N, n);
+      if constexpr (GATED) {
+        load_saved<E>(up, a.save[1], a.scale[1], a.group, row, col, a.N, n);
+        float du[V], h[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float value, slope;
+          activation_slope(pre[i], a.act, value, slope);
+          da[i] = dy.get(i) * up[i] * slope;
+          du[i] = dy.get(i) * value;
+          h[i] = value * up[i];
+        }
+        if (n > 0) {
+          if (a.da) {
+            E* out = static_cast<E*>(a.da) + row * (2 * size_t(a.N)) + col;
+            packed<E, V>(da).store(out, n);
+            packed<E, V>(du).store(out + a.N, n);
+          }
+          if (a.h) packed<E, V>(h).store(static_cast<E*>(a.h) + row * a.N + col, n);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          da[i] = dy.get(i);
+          if (a.save[0]) {
+            float value, slope;
+            activation_slope(pre[i], a.act, value, slope);
+            da[i] *= slope;
+          }
+          total[i] += da[i];
+        }
+        if (a.da && n > 0) packed<E, V>(da).store(static_cast<E*>(a.da) + row * a.N + col, n);
+      }
+    }
+  }
+  if constexpr (!GATED) {
+    if (!a.partial) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = total[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < kWave * V; c += 256) {
+      const int at = blockIdx.x % col_blocks * kWave * V + c;
+      if (at < a.N)
+        a.partial[static_cast<size_t>(strip) * a.N + at] =
+            (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+    }
+  }
+}
+
+// dbias from the strips' sums: 16 columns to a workgroup, 16 threads each.
+__global__ __launch_bounds__(256) void sum_strips_kernel(const float* partial, int strips, int N,
+                                                         float* out) {
+  __shared__ float lds[16][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int col = blockIdx.x * 16 + c;
+  float s = 0.0f;
+  if (col < N)
+    for (int i = r; i < strips; i += 16) s += partial[static_cast<size_t>(i) * N + col];
+  lds[r][c] = s;
+  __syncthreads();
+  if (r == 0 && col < N) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += lds[i][c];
+    out[col] = s;
+  }
+}
+
+// ---- checkpoints ----
+
+// A wavefront a row: with groups, scales come from the lanes of a group; with
+// one scale a row, the row is read twice (the second time from cache).
+template <typename E>
+__global__ __launch_bounds__(256) void checkpoint_save_kernel(int64_t T, int d, int group, const E* x,
+                                                              uint8_t* codes, float* scale) {
+  constexpr int V = kLaneCols<E>;
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int64_t t = int64_t(blockIdx.x) * 4 + threadIdx.x / kWave; t < T; t += int64_t(gridDim.x) * 4) {
+    const E* row = x + static_cast<size_t>(t) * d;
+    uint32_t top = 0;
+    if (group == 0) {
+      for (int c0 = 0; c0 < d; c0 += kWave * V) {
+        const int col = c0 + lane * V;
+        Pack<E, V> p;
+        p.load(row + col, there(d - col, V));
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = umax(top, size_bits(p.get(i)));
+      }
+      top = wave_max(top);
+      if (lane == 0) scale[t] = e4m3_scale(top);
+    }
+    const float inv = reciprocal(e4m3_scale(top));
+    for (int c0 = 0; c0 < d; c0 += kWave * V) {
+      const int col = c0 + lane * V;
+      const int n = there(d - col, V);
+      Pack<E, V> p;
+      p.load(row + col, n);
+      float v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = p.get(i);
+      if (group != 0) {
+        save_e4m3(v, n, codes, scale, t, col, d, group);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= inv;
+        pack_e4m3(v).store(codes + static_cast<size_t>(t) * d + col, n);
+      }
+    }
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void checkpoint_load_kernel(int64_t T, int d, int group,
+                                                              const uint8_t* codes,
+                                                              const float* scale, E* x) {
+  constexpr int V = kLaneCols<E>;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int strips = (d + kWave * V - 1) / (kWave * V);
+  for (int64_t u = int64_t(blockIdx.x) * 4 + threadIdx.x / kWave; u < T * strips;
+       u += int64_t(gridDim.x) * 4) {
+    const size_t t = static_cast<size_t>(u / strips);
+    const int col = (static_cast<int>(u % strips) * kWave + lane) * V;
+    const int n = there(d - col, V);
+    float v[V];
+    load_saved<E>(v, codes, scale, group ? group : d, t, col, d, n);
+    if (n > 0) packed<E, V>(v).store(x + t * d + col, n);
+  }
+}
+
+int64_t strips_of(int64_t T) {
+  const int64_t s = (T + kStripRows - 1) / kStripRows;
+  return s < kMaxStrips ? s : kMaxStrips;
+}
+
+template <typename E, bool GATED>
+hipError_t run_act_backward(const ActBackward& a, hipStream_t st) {
+  constexpr int kBlock = kWave * kLaneCols<E>;
+  const int64_t col_blocks = (int64_t(a.N) + kBlock - 1) / kBlock;
+  const int64_t strips = strips_of(a.T);
+  if (strips > 0) {
+    act_backward_kernel<E, GATED><<<dim3(static_cast<uint32_t>(col_blocks * strips)), dim3(256), 0, st>>>(
+        a, static_cast<int>(col_blocks), strips);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.dbias) {
+    sum_strips_kernel<<<dim3((a.N + 15) / 16), dim3(256), 0, st>>>(a.partial, static_cast<int>(strips),
+                                                                   a.N, a.dbias);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+int grid_of(int64_t units) {
+  const int64_t b = (units + 3) / 4;
+  return static_cast<int>(b < (1 << 20) ? b : (1 << 20));
+}
+
+}  // namespace
+
+size_t act_backward_partials(int64_t T, int N, bool) { return size_t(strips_of(T)) * size_t(N); }
+
+hipError_t launch_act_backward(const ActBackward& a, hipStream_t st) {
+  if (a.gated)
+    return a.bf16 ? run_act_backward<uint16_t, true>(a, st) : run_act_backward<float, true>(a, st);
+  return a.bf16 ? run_act_backward<uint16_t, false>(a, st) : run_act_backward<float, false>(a, st);
+}
+
+hipError_t launch_checkpoint_save(int64_t T, int d, bool bf16, int group, const void* x, void* codes,
+                                  float* scale, hipStream_t st) {
+  uint8_t* q = static_cast<uint8_t*>(codes);
+  if (bf16)
+    checkpoint_save_kernel<uint16_t><<<grid_of(T), 256, 0, st>>>(
+        T, d, group, static_cast<const uint16_t*>(x), q, scale);
+  else
+    checkpoint_save_kernel<float><<<grid_of(T), 256, 0, st>>>(T, d, group,
+                                                              static_cast<const float*>(x), q, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_checkpoint_load(int64_t T, int d, bool bf16, int group, const void* codes,
+                                  const float* scale, void* x, hipStream_t st) {
+  const uint8_t* q = static_cast<const uint8_t*>(codes);
+  const int cols = kWave * (bf16 ? 8 : 4);
+  const int grid = grid_of(T * ((int64_t(d) + cols - 1) / cols));
+  if (bf16)
+    checkpoint_load_kernel<uint16_t><<<grid, 256, 0, st>>>(T, d, group, q, scale,
+                                                           static_cast<uint16_t*>(x));
+  else
+    checkpoint_load_kernel<float><<<grid, 256, 0, st>>>(T, d, group, q, scale, static_cast<float*>(x));
+  return hipGetLastError();
+}
+
+}  // namespace fff

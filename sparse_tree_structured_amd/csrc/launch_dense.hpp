@@ -1,0 +1,87 @@
+// Host-side launchers of the dense feed-forward kernels: matrix products with
+// an epilogue, the elementwise part of their backward passes, and activation
+// checkpoints in 8 bits.  Each enqueues its kernel(s) on `st` and returns
+// hipGetLastError().  Arguments have been validated by the C-ABI layer before
+// any of these is called.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace fff {
+
+// C[M,N] = A . B over K.  An operand is held with K contiguous in its rows,
+// or k-major (row k holds consecutive rows of A or columns of B).
+enum ProductKind {
+  kProductNN,  // A rows, B k-major:     x . W
+  kProductNT,  // A rows, B rows:        da . W^T
+  kProductTN,  // A k-major, B k-major:  x^T . da
+};
+
+// Products with two B operands of the same sizes.
+enum ProductPair {
+  kSingle,
+  kPairColumns,  // A . B0 and A . B1 in one workgroup: the gated pair
+  kPairSum,      // A . B0 + (A + a_second) . B1: the gated pair's dx
+  kPairTwo,      // A . B0 and A . B1 as products of their own: its weights' gradients
+};
+
+// What becomes of 32-bit sums v (and, of the gated pair, w).
+struct Epilogue {
+  int64_t M;
+  int N;
+  int act;              // fff_act_t
+  const void* bias;     // layer type [N], or null
+  const void* residual;  // output type [M,N], or null
+  void* out[2];         // [M,N]; the second one of kPairTwo
+  void* save[2];        // [M,N] v and w as they are before the activation, or null
+  float* scale[2];      // [M, groups] of 8-bit saves; null: saved in the layer's type
+  int group;            // columns of a scale
+};
+
+struct Product {
+  ProductKind kind;
+  ProductPair pair;
+  bool bf16;      // A, B, bias and saves; else float32
+  bool out_bf16;  // out and residual
+  const void *a, *b[2];
+  int64_t lda, ldb;    // elements from a row to the next
+  int64_t a_second;    // kPairSum: elements from A to the second segment's A
+  int64_t M;
+  int N;
+  int64_t K;      // of one product
+  Epilogue e;
+};
+
+// Whether its tiles fit one launch.
+bool product_fits(const Product& p);
+// Workspace of a product: its partial sums where it is cut along K.
+size_t product_workspace(const Product& p);
+hipError_t launch_product(const Product& p, void* workspace, hipStream_t st);
+
+// Elementwise part of the backward passes, and column sums.
+struct ActBackward {
+  int64_t T;
+  int N;
+  bool bf16;
+  bool gated;
+  int act;
+  const void* dy;         // [T,N]
+  const void* save[2];    // pre-activation (gated: gate, up), or null where act is none
+  const float* scale[2];  // of 8-bit saves, or null
+  int group;
+  void* da;               // [T,N], gated [T,2N] (gate's gradient, then up's); or null
+  void* h;                // gated: act(gate) * up [T,N], or null
+  float* dbias;           // [N] sums over rows of da, or null
+  float* partial;         // workspace of dbias
+};
+size_t act_backward_partials(int64_t T, int N, bool bf16);  // floats
+hipError_t launch_act_backward(const ActBackward& a, hipStream_t st);
+
+hipError_t launch_checkpoint_save(int64_t T, int d, bool bf16, int group, const void* x, void* codes,
+                                  float* scale, hipStream_t st);
+hipError_t launch_checkpoint_load(int64_t T, int d, bool bf16, int group, const void* codes,
+                                  const float* scale, void* x, hipStream_t st);
+
+}  // namespace fff
