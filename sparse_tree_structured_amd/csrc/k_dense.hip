@@ -1,10 +1,6 @@
-// Matrix products of the dense feed-forward block: choice of kernel, slices
-// of K and their sums.
-#include <type_traits>
-
-#include "dense.hpp"
-#include "dense_any.hpp"
-#include "launch.hpp"
+// Matrix products of the dense feed-forward block: how one is cut into tiles
+// and slices of K, and the sums of the slices.
+#include "product.hpp"
 
 namespace fff {
 namespace {
@@ -45,110 +41,125 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(const float* partial, i
   }
 }
 
-template <typename E> using TileAny = AnyCfg<E, 128, 256, 64, 64>;
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Whether the rows of both operands are whole 16-byte pieces.
+bool direct_sizes(const Product& p) {
+  if (!p.bf16 || p.lda % 8 != 0 || p.ldb % 8 != 0 || p.a_second % 8 != 0) return false;
+  return p.kind == kProductTN || p.K % 8 == 0;
+}
 
-// How a product is cut.
-struct Cut {
-  int64_t tiles_m, tiles_n;
-  int products;  // sums of a slice in the workspace
-  int slices, steps;
+struct TileSize {
+  ProductTile tile;
+  int m, n, bk;
+  double rate;  // of its matrix-core work, FLOP/s of a compute unit
 };
 
-// Slices of K while the tiles leave compute units idle: as many as fill the
-// chip once, of at least 8 steps each.
-Cut cut_any(const Product& p) {
-  const int bk = p.bf16 ? 32 : 16;
+// The time of a product in one kind of tile and number of slices, in us: what
+// the busiest compute unit does, a start and an epilogue for each of its
+// tiles, and for slices a second launch and the sums' way through memory.
+double time_of(const Product& p, const TileSize& t, int64_t tiles, int64_t total, int64_t slices) {
+  const int64_t steps = ceil_div(total, slices);
+  const int64_t rounds = ceil_div(tiles * slices, 256);
+  const double step = 2.0 * t.m * t.n * t.bk / t.rate * 1e6;
+  double us = rounds * (steps * (step > 0.25 ? step : 0.25) + 4.0);
+  if (slices > 1) {
+    const int products = p.pair == kPairColumns || p.pair == kPairTwo ? 2 : 1;
+    us += 3.0 + 8.0 * slices * products * p.M * p.N / 4e6;
+  }
+  return us;
+}
+
+Cut cut_with(const Product& p, const TileSize& t, double& us) {
   Cut c;
-  const int cols = p.pair == kPairColumns ? 128 : 256;
-  c.tiles_m = ceil_div(p.M, 128);
-  c.tiles_n = ceil_div(p.N, cols);
+  c.tile = t.tile;
+  c.tiles_m = ceil_div(p.M, t.m);
+  c.tiles_n = ceil_div(p.N, p.pair == kPairColumns ? t.n / 2 : t.n);
   c.products = p.pair == kPairColumns || p.pair == kPairTwo ? 2 : 1;
   int64_t tiles = c.tiles_m * c.tiles_n * (p.pair == kPairTwo ? 2 : 1);
   if (tiles < 1) tiles = 1;
-  const int64_t total = ceil_div(p.K, bk) * (p.pair == kPairSum ? 2 : 1);
+  const int64_t total = ceil_div(p.K, t.bk) * (p.pair == kPairSum ? 2 : 1);
   int64_t slices = 1;
-  if (tiles < 192) {
-    slices = 256 / tiles;
-    if (slices > total / 8) slices = total / 8;
-    if (slices < 1) slices = 1;
+  us = time_of(p, t, tiles, total, 1);
+  // Slices of at least four steps while tiles leave compute units idle.
+  for (int64_t s = 2; s * tiles <= 512 && s * 4 <= total; ++s) {
+    const double with = time_of(p, t, tiles, total, s);
+    if (with < us) us = with, slices = s;
   }
   c.steps = static_cast<int>(ceil_div(total, slices));
   c.slices = total > 0 ? static_cast<int>(ceil_div(total, c.steps)) : 1;
   return c;
 }
 
-template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
-hipError_t run_any(const Product& p, const Epi& epi, const Cut& c, hipStream_t st) {
-  using Cfg = TileAny<E>;
-  auto kern = product_any_kernel<E, KIND, PAIR, Cfg, Epi>;
-  constexpr size_t lds = AnyParts<E, KIND, PAIR == kPairColumns, Cfg>::kLds;
-  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), static_cast<int>(lds));
-  if (e != hipSuccess) return e;
-  const int64_t blocks = c.tiles_m * c.tiles_n * c.slices * (PAIR == kPairTwo ? 2 : 1);
-  kern<<<dim3(static_cast<uint32_t>(blocks)), dim3(Cfg::kThreads), lds, st>>>(
-      p, epi, static_cast<int>(c.tiles_m), static_cast<int>(c.tiles_n), c.steps);
-  return hipGetLastError();
-}
-
-template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
-hipError_t run_with(const Product& p, const Epi& epi, void* workspace, hipStream_t st) {
-  const Cut c = cut_any(p);
-  if (c.slices <= 1) return run_any<E, KIND, PAIR>(p, epi, c, st);
-  PartialEpilogue<Epi::kGated> part;
-  part.partial = static_cast<float*>(workspace);
-  part.M = p.M;
-  part.N = p.N;
-  part.products = c.products;
-  const hipError_t e = run_any<E, KIND, PAIR>(p, part, c, st);
-  if (e != hipSuccess) return e;
-  const int64_t units = p.M * ceil_div(p.N, 256) * (Epi::kGated ? 1 : c.products);
-  const int64_t blocks = ceil_div(units, 4);
-  sum_slices_kernel<Epi><<<dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
-                           st>>>(part.partial, c.slices, c.products, p.M, p.N, epi);
-  return hipGetLastError();
-}
-
-template <typename E, ProductKind KIND, ProductPair PAIR>
-hipError_t run_linear(const Product& p, void* workspace, hipStream_t st) {
-  if constexpr (sizeof(E) == 2) {
-    if (p.out_bf16) return run_with<E, KIND, PAIR>(p, LinearEpilogue<E, uint16_t>{p.e}, workspace, st);
+Cut cut_direct(const Product& p) {
+  static const TileSize kTiles[] = {{kTileBig, 256, 256, 32, 4.4e12},
+                                    {kTileMid, 128, 256, 32, 3.6e12},
+                                    {kTileSmall, 128, 128, 32, 3.2e12}};
+  Cut best = {};
+  double least = 0;
+  for (const TileSize& t : kTiles) {
+    if (t.tile == kTileSmall && p.pair == kPairColumns) continue;
+    double us;
+    const Cut c = cut_with(p, t, us);
+    if (t.tile == kTileBig || us < least) best = c, least = us;
   }
-  return run_with<E, KIND, PAIR>(p, LinearEpilogue<E, float>{p.e}, workspace, st);
+  return best;
 }
 
-template <typename E>
-hipError_t run_product(const Product& p, void* workspace, hipStream_t st) {
-  if (p.kind == kProductNN) {
-    if (p.pair == kPairColumns)
-      return run_with<E, kProductNN, kPairColumns>(p, GatedEpilogue<E>{p.e}, workspace, st);
-    return run_linear<E, kProductNN, kSingle>(p, workspace, st);
-  }
-  if (p.kind == kProductNT) {
-    if (p.pair == kPairSum) return run_linear<E, kProductNT, kPairSum>(p, workspace, st);
-    return run_linear<E, kProductNT, kSingle>(p, workspace, st);
-  }
-  if (p.pair == kPairTwo) return run_linear<E, kProductTN, kPairTwo>(p, workspace, st);
-  return run_linear<E, kProductTN, kSingle>(p, workspace, st);
+Cut cut_any(const Product& p) {
+  double us;
+  return cut_with(p, {kTileAny, 128, 256, p.bf16 ? 32 : 16, p.bf16 ? 3e12 : 0.4e12}, us);
 }
 
-}  // namespace
-
-bool product_fits(const Product& p) {
-  const Cut c = cut_any(p);
-  // (a launch has fewer than 2^32 threads)
-  return c.tiles_m * c.tiles_n * c.slices * 2 < (int64_t(1) << 23);
-}
-
-size_t product_workspace(const Product& p) {
-  const Cut c = cut_any(p);
+size_t cut_bytes(const Product& p, const Cut& c) {
   return c.slices <= 1 ? 0
                        : size_t(c.slices) * c.products * size_t(p.M) * size_t(p.N) * sizeof(float);
 }
 
+}  // namespace
+
+template <class Epi>
+hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int N, const Epi& epi,
+                             hipStream_t st) {
+  const int64_t units = M * ceil_div(N, 256) * (Epi::kGated ? 1 : c.products);
+  const int64_t blocks = ceil_div(units, 4);
+  sum_slices_kernel<Epi><<<dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
+                           st>>>(partial, c.slices, c.products, M, N, epi);
+  return hipGetLastError();
+}
+#define FFF_SUM(E)                                                                                \
+  template hipError_t launch_sum_slices<E>(const float*, const Cut&, int64_t, int, const E&, \
+                                           hipStream_t)
+FFF_SUM(GatedEpilogue<uint16_t>);
+FFF_SUM(GatedEpilogue<float>);
+using LinearBf16 = LinearEpilogue<uint16_t, uint16_t>;
+using LinearMixed = LinearEpilogue<uint16_t, float>;
+using LinearF32 = LinearEpilogue<float, float>;
+FFF_SUM(LinearBf16);
+FFF_SUM(LinearMixed);
+FFF_SUM(LinearF32);
+
+Cut cut_product(const Product& p) {
+  const bool direct = direct_sizes(p) && aligned16(p.a) && aligned16(p.b[0]) && aligned16(p.b[1]);
+  return direct ? cut_direct(p) : cut_any(p);
+}
+
+bool product_fits(const Product& p) {
+  const Cut c = cut_any(p);
+  // (a launch has fewer than 2^32 threads)
+  return c.tiles_m * c.tiles_n * c.slices * 2 < (int64_t(1) << 22);
+}
+
+// For pointers of any alignment.
+size_t product_workspace(const Product& p) {
+  const size_t any = cut_bytes(p, cut_any(p));
+  const size_t direct = direct_sizes(p) ? cut_bytes(p, cut_direct(p)) : 0;
+  return any > direct ? any : direct;
+}
+
 hipError_t launch_product(const Product& p, void* workspace, hipStream_t st) {
-  return p.bf16 ? run_product<uint16_t>(p, workspace, st) : run_product<float>(p, workspace, st);
+  if (p.kind == kProductNN) return run_nn(p, workspace, st);
+  return p.kind == kProductNT ? run_nt(p, workspace, st) : run_tn(p, workspace, st);
 }
 
 }  // namespace fff

@@ -1,0 +1,94 @@
+// How a product is cut and launched; one translation unit for each kind.
+#pragma once
+
+#include <type_traits>
+
+#include "dense.hpp"
+#include "dense_any.hpp"
+#include "dense_direct.hpp"
+#include "launch.hpp"
+
+namespace fff {
+
+// Kernels: register staged (any sizes, types and alignment), or straight into
+// LDS with tiles of 256 x 256, 128 x 256 or 128 x 128.
+enum ProductTile { kTileAny, kTileBig, kTileMid, kTileSmall };
+
+struct Cut {
+  ProductTile tile;
+  int64_t tiles_m, tiles_n;
+  int products;       // sums of a slice in the workspace
+  int slices, steps;  // of K
+};
+Cut cut_product(const Product& p);
+
+template <typename E> using TileAny = AnyCfg<E, 128, 256, 64, 64>;
+using TileBig = DirectCfg<256, 256, 128, 64, 4>;
+using TileMid = DirectCfg<128, 256, 64, 64, 4>;
+using TileSmall = DirectCfg<128, 128, 64, 64, 4>;  // two workgroups a compute unit
+
+template <class Epi>
+hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int N, const Epi& epi,
+                             hipStream_t st);
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <class Kernel, class Epi>
+hipError_t launch_tiles(Kernel kern, size_t lds, int threads, const Product& p, const Epi& epi,
+                        const Cut& c, hipStream_t st) {
+  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), static_cast<int>(lds));
+  if (e != hipSuccess) return e;
+  const int64_t blocks = c.tiles_m * c.tiles_n * c.slices * (p.pair == kPairTwo ? 2 : 1);
+  kern<<<dim3(static_cast<uint32_t>(blocks)), dim3(threads), lds, st>>>(
+      p, epi, static_cast<int>(c.tiles_m), static_cast<int>(c.tiles_n), c.steps);
+  return hipGetLastError();
+}
+
+template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
+hipError_t launch_cut(const Product& p, const Epi& epi, const Cut& c, hipStream_t st) {
+  constexpr bool kTwo = PAIR == kPairColumns;
+  if constexpr (sizeof(E) == 2) {
+    auto direct = [&](auto cfg) {
+      using C = decltype(cfg);
+      return launch_tiles(product_direct_kernel<KIND, PAIR, C, Epi>, DirectParts<KIND, kTwo, C>::kLds,
+                          C::kThreads, p, epi, c, st);
+    };
+    if (c.tile == kTileBig) return direct(TileBig());
+    if (c.tile == kTileMid) return direct(TileMid());
+    if constexpr (!kTwo) {
+      if (c.tile == kTileSmall) return direct(TileSmall());
+    }
+  }
+  using C = TileAny<E>;
+  return launch_tiles(product_any_kernel<E, KIND, PAIR, C, Epi>, AnyParts<E, KIND, kTwo, C>::kLds,
+                      C::kThreads, p, epi, c, st);
+}
+
+template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
+hipError_t run_with(const Product& p, const Epi& epi, void* workspace, hipStream_t st) {
+  const Cut c = cut_product(p);
+  if (c.slices <= 1) return launch_cut<E, KIND, PAIR>(p, epi, c, st);
+  PartialEpilogue<Epi::kGated> part;
+  part.partial = static_cast<float*>(workspace);
+  part.M = p.M;
+  part.N = p.N;
+  part.products = c.products;
+  const hipError_t e = launch_cut<E, KIND, PAIR>(p, part, c, st);
+  if (e != hipSuccess) return e;
+  return launch_sum_slices(part.partial, c, p.M, p.N, epi, st);
+}
+
+// Out and residual in the layer's type or in 32 bits.
+template <typename E, ProductKind KIND, ProductPair PAIR>
+hipError_t run_linear(const Product& p, void* workspace, hipStream_t st) {
+  if constexpr (sizeof(E) == 2) {
+    if (p.out_bf16) return run_with<E, KIND, PAIR>(p, LinearEpilogue<E, uint16_t>{p.e}, workspace, st);
+  }
+  return run_with<E, KIND, PAIR>(p, LinearEpilogue<E, float>{p.e}, workspace, st);
+}
+
+hipError_t run_nn(const Product& p, void* workspace, hipStream_t st);
+hipError_t run_nt(const Product& p, void* workspace, hipStream_t st);
+hipError_t run_tn(const Product& p, void* workspace, hipStream_t st);
+
+}  // namespace fff
