@@ -191,8 +191,8 @@ struct PartialEpilogue {
 // epilogue, a band of 32 rows of every wavefront row at a time, so that the
 // lanes of a wavefront have consecutive columns: residuals are read and
 // outputs written in whole lines, and an 8-bit save's groups are at hand.
-// GATED: a wavefront's column block j = 0 is of v, j = 1 of w, 32 columns
-// each.
+// GATED: the first half of a wavefront's column blocks is of v, the second
+// of w.
 template <class C>
 constexpr int band_pitch() { return C::BN + 4; }  // floats
 template <class C>
@@ -206,9 +206,9 @@ __device__ __forceinline__ void tile_epilogue(const f32x16_t (&acc)[C::kTm][C::k
   constexpr int kPitch = band_pitch<C>();
   constexpr int kCols = G ? C::BN / 2 : C::BN;  // output columns of the tile
   constexpr int kRowsAtOnce = C::kThreads * 4 / kCols;
-  constexpr int kRounds = C::kWavesM * 32 / kRowsAtOnce;
-  static_assert(kCols >= 128 && C::kWavesM * 32 % kRowsAtOnce == 0, "bands in whole rounds");
-  static_assert(!G || (C::kTn == 2 && C::WN == 64), "gated column blocks");
+  constexpr int kRounds = 4;  // at a time
+  constexpr int kBandRows = C::kWavesM * 32;
+  static_assert(kCols >= 128 && kBandRows % (kRowsAtOnce * kRounds) == 0, "bands in whole rounds");
   float* band = reinterpret_cast<float*>(lds);
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
@@ -219,23 +219,15 @@ __device__ __forceinline__ void tile_epilogue(const f32x16_t (&acc)[C::kTm][C::k
   const int col = n0 + c4;
   typename Epi::Column column;
   epi.column(column, col);
+  const int left = N - col;
+  const int n_col = left < 0 ? 0 : left < 4 ? left : 4;
 #pragma unroll
   for (int i = 0; i < C::kTm; ++i) {
-    typename Epi::Early early[kRounds];
-    int ns[kRounds];
-    int64_t rows[kRounds];
-#pragma unroll
-    for (int u = 0; u < kRounds; ++u) {
-      const int b = tid / (kCols / 4) + u * kRowsAtOnce;
-      rows[u] = m0 + (b / 32) * C::WM + i * 32 + b % 32;
-      const int left = N - col;
-      ns[u] = rows[u] < M ? (left < 0 ? 0 : left < 4 ? left : 4) : 0;
-      epi.early(early[u], rows[u], col, ns[u]);
-    }
     __syncthreads();  // the stages, or the previous band, have been read
 #pragma unroll
     for (int j = 0; j < C::kTn; ++j) {
-      const int cj = G ? j * (C::BN / 2) + wn * 32 : wn * C::WN + j * 32;
+      const int cj = G ? j / (C::kTn / 2) * (C::BN / 2) + wn * (C::WN / 2) + j % (C::kTn / 2) * 32
+                       : wn * C::WN + j * 32;
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<float4*>(band + (wm * 32 + (lane & 31)) * kPitch + cj + g * 8 +
@@ -244,17 +236,27 @@ __device__ __forceinline__ void tile_epilogue(const f32x16_t (&acc)[C::kTm][C::k
                         acc[i][j][4 * g + 3]);
     }
     __syncthreads();
+    for (int u0 = 0; u0 < kBandRows; u0 += kRowsAtOnce * kRounds) {
+      typename Epi::Early early[kRounds];
+      auto row_of = [&](int u) {
+        const int b = tid / (kCols / 4) + u0 + u * kRowsAtOnce;
+        return m0 + (b / 32) * C::WM + i * 32 + b % 32;
+      };
 #pragma unroll
-    for (int u = 0; u < kRounds; ++u) {
-      const int b = tid / (kCols / 4) + u * kRowsAtOnce;
-      const float4 p = *reinterpret_cast<const float4*>(band + b * kPitch + c4);
-      const float v[4] = {p.x, p.y, p.z, p.w};
-      float w[4] = {};
-      if constexpr (G) {
-        const float4 q = *reinterpret_cast<const float4*>(band + b * kPitch + C::BN / 2 + c4);
-        w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+      for (int u = 0; u < kRounds; ++u)
+        epi.early(early[u], row_of(u), col, row_of(u) < M ? n_col : 0);
+#pragma unroll
+      for (int u = 0; u < kRounds; ++u) {
+        const int b = tid / (kCols / 4) + u0 + u * kRowsAtOnce;
+        const float4 p = *reinterpret_cast<const float4*>(band + b * kPitch + c4);
+        const float v[4] = {p.x, p.y, p.z, p.w};
+        float w[4] = {};
+        if constexpr (G) {
+          const float4 q = *reinterpret_cast<const float4*>(band + b * kPitch + C::BN / 2 + c4);
+          w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+        }
+        epi.apply(column, early[u], row_of(u), col, row_of(u) < M ? n_col : 0, v, w, which);
       }
-      epi.apply(column, early[u], rows[u], col, ns[u], v, w, which);
     }
   }
 }

@@ -29,8 +29,14 @@ struct Stager {
   static_assert(sizeof(E) == 4 || L == kRows || OUTER % 128 == 0, "swizzle spans 16 chunks");
   Pack<E, V> r[kChunks];
 
+  // (rows of 128 bytes have eight chunks: 16 rows' reads of one chunk cover
+  // all banks with the row's bits 1 to 3, as with bits 2 and 3 for 64 bytes)
+  static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (L == kKMajor) return (row & 3) << 2;
+    return BK == 64 ? (row >> 1) & 7 : lds_swz(row);
+  }
   static __device__ __forceinline__ int slot(int row, int chunk) {
-    if constexpr (sizeof(E) == 2) chunk ^= L == kRows ? lds_swz(row) : (row & 3) << 2;
+    if constexpr (sizeof(E) == 2) chunk ^= swizzle(row);
     return (row * kPitch + chunk * V) * int(sizeof(E));
   }
   // p: element (first row or column, k = 0); outer_left, k_left: how many there are.

@@ -30,21 +30,45 @@ __device__ __forceinline__ void dma16_base(const void* base, uint32_t offset, ui
       : "memory");
 }
 
+// Tiles of BM x BN, a wavefront WM x WN of them, K steps of BK_ in STAGES
+// stages.
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int STAGES_>
+struct StepCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_;
+  static constexpr int kStages = STAGES_;
+  static constexpr int kWavesM = BM / WM, kWavesN = BN / WN, kWaves = kWavesM * kWavesN;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int kTm = WM / 32, kTn = WN / 32;
+  static constexpr int kStageBytes = (BM + BN) * BK * 2;
+  static constexpr size_t kLdsBytes = size_t(kStages) * kStageBytes;
+  static constexpr int kALoads = BM * BK / 512 / kWaves;  // 1 KB copies of a wavefront and stage
+  static constexpr int kBLoads = BN * BK / 512 / kWaves;
+  static_assert(BM * BK % (512 * kWaves) == 0 && BN * BK % (512 * kWaves) == 0, "whole copies");
+  static_assert((BK == 32 && kStages >= 3) || (BK == 64 && kStages == 2), "the two schedules below");
+};
+
+// f(0), f(1), ... f(N - 1) with constants.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(const F& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each<N, I + 1>(f);
+  }
+}
+
 // Where a lane's 16 bytes of 1 KB piece q of a stage's block of OUTER rows
-// (or columns) by 32 of K come from: rows (or columns) outer, K from k on.
-template <int OUTER, Layout L>
+// (or columns) by BK of K come from: rows (or columns) outer, K from k on.
+template <int OUTER, int BK, Layout L>
 struct PieceAt {
   int outer, k;
   __device__ __forceinline__ PieceAt(int q, int lane) {
-    if constexpr (L == kRows) {
-      outer = q * 16 + (lane >> 2);
-      k = ((lane & 3) ^ lds_swz(outer)) * 8;
-    } else {
-      constexpr int kRow = OUTER * 2;
-      const int byte = q * 1024 + lane * 16;
-      k = byte / kRow;
-      outer = (((byte % kRow) >> 4) ^ ((k & 3) << 2)) * 8;
-    }
+    using S = Stager<uint16_t, OUTER, BK, L, OUTER * BK / 8>;
+    constexpr int kRow = L == kRows ? BK * 2 : OUTER * 2;
+    const int byte = q * 1024 + lane * 16;
+    const int row = byte / kRow;
+    const int e = (((byte % kRow) >> 4) ^ S::swizzle(row)) * 8;
+    outer = L == kRows ? row : e;
+    k = L == kRows ? e : row;
   }
   // Bytes from the block's first element; what is past the operand's end is
   // read from its last row, or its first columns, and not used.
@@ -64,11 +88,13 @@ struct DirectParts {
   static constexpr Layout kB = KIND == kProductNT ? kRows : kKMajor;
   static constexpr int kBlocks = PAIR ? 2 : 1;
   static constexpr int kBCols = C::BN / kBlocks;
-  static constexpr int kBPieces = kBCols / 16;  // of one block
-  using SA = Stager<uint16_t, C::BM, 32, kA, C::BM * 4>;
-  using SB = Stager<uint16_t, kBCols, 32, kB, kBCols * 4>;
+  static constexpr int kBPieces = kBCols * C::BK / 512;  // of one block
+  using SA = Stager<uint16_t, C::BM, C::BK, kA, C::BM * C::BK / 8>;
+  using SB = Stager<uint16_t, kBCols, C::BK, kB, kBCols * C::BK / 8>;
+  using PA = PieceAt<C::BM, C::BK, kA>;
+  using PB = PieceAt<kBCols, C::BK, kB>;
   static constexpr size_t kLds = C::kLdsBytes > band_bytes<C>() ? C::kLdsBytes : band_bytes<C>();
-  static_assert(SA::kBytes == C::BM * 64 && SB::kBytes == kBCols * 64, "stage blocks");
+  static_assert(SA::kBytes == C::BM * C::BK * 2 && SB::kBytes == kBCols * C::BK * 2, "stage blocks");
 };
 
 template <ProductKind KIND, ProductPair PAIR, class C, class Epi>
@@ -91,85 +117,158 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
   uint32_t a_off[C::kALoads], b_off[C::kBLoads];
 #pragma unroll
   for (int j = 0; j < C::kALoads; ++j)
-    a_off[j] = PieceAt<C::BM, P::kA>(wave * C::kALoads + j, lane).offset(p.lda, p.M - m0);
+    a_off[j] = typename P::PA(wave * C::kALoads + j, lane).offset(p.lda, p.M - m0);
 #pragma unroll
   for (int j = 0; j < C::kBLoads; ++j)
-    b_off[j] = PieceAt<P::kBCols, P::kB>((wave * C::kBLoads + j) % P::kBPieces, lane)
-                   .offset(p.ldb, p.N - n0);
-  const int64_t a_step = P::kA == kRows ? 64 : p.lda * 64;  // bytes from a step to the next
-  const int64_t b_step = P::kB == kRows ? 64 : p.ldb * 64;
+    b_off[j] = typename P::PB((wave * C::kBLoads + j) % P::kBPieces, lane).offset(p.ldb, p.N - n0);
+  const int64_t a_step = P::kA == kRows ? C::BK * 2 : p.lda * (C::BK * 2);  // bytes from a step to the next
+  const int64_t b_step = P::kB == kRows ? C::BK * 2 : p.ldb * (C::BK * 2);
   const unsigned char* a0 =
       static_cast<const unsigned char*>(p.a) + 2 * (P::kA == kRows ? m0 * p.lda : m0);
   const int64_t b0 = 2 * (P::kB == kRows ? int64_t(n0) * p.ldb : n0);
-  const int per = static_cast<int>((p.K + 31) / 32);  // steps of one segment
+  const int per = static_cast<int>((p.K + C::BK - 1) / C::BK);  // steps of one segment
   const int total = PAIR == kPairSum ? 2 * per : per;
   const int first = at.slice * steps;
   const int nk = (first + steps < total ? first + steps : total) - first;
 
-  auto issue = [&](int s) {
+  // Where the copies of a stage come from and go to, the same for all lanes.
+  struct From {
+    const unsigned char *a, *b0, *b1;
+    uint32_t to;
+    int k_left;
+  };
+  auto from = [&](int s) __attribute__((always_inline)) {
     const int ks = first + s;
     const int seg = PAIR == kPairSum && ks >= per ? 1 : 0;
     const int k = ks - seg * per;
-    const unsigned char* a = a0 + k * a_step + (PAIR == kPairSum ? seg * p.a_second * 2 : 0);
-    const int64_t k_left = p.K - int64_t(k) * 32;
-    const uint32_t stage = lds_at + (s % S) * C::kStageBytes;
-    auto copy = [&](const void* base, uint32_t offset, uint32_t to, bool there) {
-      if (k_left >= 32) {
+    From f;
+    f.a = a0 + k * a_step + (PAIR == kPairSum ? seg * p.a_second * 2 : 0);
+    const int64_t b = b0 + k * b_step;
+    const bool second = PAIR == kPairSum ? seg != 0 : PAIR == kPairTwo && at.which != 0;
+    f.b0 = static_cast<const unsigned char*>(second ? p.b[1] : p.b[0]) + b;
+    f.b1 = kTwo ? static_cast<const unsigned char*>(p.b[1]) + b : nullptr;
+    f.to = lds_at + (s % S) * C::kStageBytes;
+    f.k_left = static_cast<int>(p.K) - k * C::BK;
+    return f;
+  };
+  // Copy j (of kPerStage) of a wavefront; TAIL: the operands end in the stage.
+  auto issue = [&](const From& f, auto copy_j, auto tail) __attribute__((always_inline)) {
+    constexpr int j = decltype(copy_j)::value;
+    auto copy = [&](const unsigned char* base, uint32_t offset, uint32_t to, int piece_k)
+        __attribute__((always_inline)) {
+      if constexpr (!decltype(tail)::value) {
         dma16_base(base, offset, to);
       } else {
-        const unsigned char* from = static_cast<const unsigned char*>(base) + offset;
-        if (!there) from = kZeros;
-        dma16_asm(from, reinterpret_cast<unsigned char*>(static_cast<uintptr_t>(to)));
+        const unsigned char* at = piece_k < f.k_left ? base + offset : kZeros;
+        dma16_asm(at, reinterpret_cast<unsigned char*>(static_cast<uintptr_t>(to)));
       }
     };
-#pragma unroll
-    for (int j = 0; j < C::kALoads; ++j) {
+    if constexpr (j < C::kALoads) {
       const int q = wave * C::kALoads + j;
-      copy(a, a_off[j], stage + q * 1024, PieceAt<C::BM, P::kA>(q, lane).k < k_left);
-    }
-#pragma unroll
-    for (int j = 0; j < C::kBLoads; ++j) {
-      const int q = wave * C::kBLoads + j;
-      const int which = PAIR == kPairSum ? seg : PAIR == kPairTwo ? at.which : q / P::kBPieces;
-      const unsigned char* b =
-          static_cast<const unsigned char*>(which ? p.b[1] : p.b[0]) + b0 + k * b_step;
-      copy(b, b_off[j], stage + C::BM * 64 + q * 1024,
-           PieceAt<P::kBCols, P::kB>(q % P::kBPieces, lane).k < k_left);
+      copy(f.a, a_off[j], f.to + q * 1024, typename P::PA(q, lane).k);
+    } else {
+      const int q = wave * C::kBLoads + j - C::kALoads;
+      copy(kTwo && q >= P::kBPieces ? f.b1 : f.b0, b_off[j - C::kALoads],
+           f.to + P::SA::kBytes + q * 1024, typename P::PB(q % P::kBPieces, lane).k);
     }
   };
-  auto read = [&](Frags<C>& f, int s, int kk) {
+  auto issue_all = [&](int s) __attribute__((always_inline)) {
+    const From f = from(s);
+    if (f.k_left >= C::BK)
+      each<kPerStage>([&](auto j) __attribute__((always_inline)) { issue(f, j, std::false_type()); });
+    else
+      each<kPerStage>([&](auto j) __attribute__((always_inline)) { issue(f, j, std::true_type()); });
+  };
+  // Fragment n (of kFrags) of step kk of stage s, in the order of their first use.
+  constexpr int kFrags = C::kTm + C::kTn;
+  auto read = [&](Frags<C>& f, int s, int kk, auto frag_n) __attribute__((always_inline)) {
+    constexpr int n = decltype(frag_n)::value;
     const unsigned char* As = lds + (s % S) * C::kStageBytes;
-    const unsigned char* Bs = As + C::BM * 64;
-#pragma unroll
-    for (int i = 0; i < C::kTm; ++i)
+    const unsigned char* Bs = As + P::SA::kBytes;
+    if constexpr (n < C::kTn) {
+      f.b[n] = frag_bf16<typename P::SB, P::kB>(
+          Bs + (kTwo ? n / (C::kTn / 2) * P::SB::kBytes : 0),
+          kTwo ? wn * (C::WN / 2) + n % (C::kTn / 2) * 32 : wn * C::WN + n * 32, kk, lane);
+    } else {
+      const int i = n - C::kTn;
       f.a[i] = frag_bf16<typename P::SA, P::kA>(As, wm * C::WM + i * 32, kk, lane);
-#pragma unroll
-    for (int j = 0; j < C::kTn; ++j)
-      f.b[j] = frag_bf16<typename P::SB, P::kB>(Bs + (kTwo ? j * P::SB::kBytes : 0),
-                                               kTwo ? wn * 32 : wn * C::WN + j * 32, kk, lane);
+    }
   };
 
   f32x16_t acc[C::kTm][C::kTn];
   zero_acc<C>(acc);
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s)
-    if (s < nk) issue(s);
-  wait_stages<kPerStage, S - 2>(nk - 1);
-  stage_barrier();
   Frags<C> f0, f1;
-  read(f0, 0, 0);
-  for (int s = 0; s < nk; ++s) {
-    read(f1, s, 1);
-    asm volatile("" ::: "memory");
-    mma_frags<C>(acc, f0);
-    if (s + 1 < nk) {
-      wait_stages<kPerStage, S - 3>(nk - 2 - s);
-      stage_barrier();
-      if (s + S - 1 < nk) issue(s + S - 1);
+  // The matrix-core operations of one step of 16, with the fragments of the
+  // next step read between them, and copies between those: bunched up, either
+  // leaves the matrix cores without work while it is issued.
+  constexpr int kMma = C::kTm * C::kTn;
+  enum { kNoCopies, kWholeCopies, kAnyCopies };  // any: a stage with a tail, or none
+  using None = std::integral_constant<int, kNoCopies>;
+  using Whole = std::integral_constant<int, kWholeCopies>;
+  using Any = std::integral_constant<int, kAnyCopies>;
+  auto phase = [&](const Frags<C>& f, Frags<C>& next, int rs, int rkk, int cs, auto copies)
+      __attribute__((always_inline)) {
+    constexpr int kCopies = decltype(copies)::value;
+    From stage;
+    if constexpr (kCopies != kNoCopies) stage = from(cs);
+    each<kMma>([&](auto m) __attribute__((always_inline)) {
+      constexpr int i = m / C::kTn, j = m % C::kTn;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+      each<kFrags>([&](auto n) __attribute__((always_inline)) {
+        if constexpr (n * kMma / kFrags == m) read(next, rs, rkk, n);
+      });
+      each<kPerStage>([&](auto c) __attribute__((always_inline)) {
+        if constexpr (kCopies == kWholeCopies && c * kMma / kPerStage == m)
+          issue(stage, c, std::false_type());
+        if constexpr (kCopies == kAnyCopies && c * kMma / kPerStage == m)
+          if (cs < nk) issue(stage, c, std::true_type());
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  auto read_all = [&](Frags<C>& f, int s, int kk) __attribute__((always_inline)) {
+    each<kFrags>([&](auto n) __attribute__((always_inline)) { read(f, s, kk, n); });
+  };
+  constexpr int kAhead = C::BK == 32 ? S - 1 : 2;  // stage s fills stage s + kAhead's buffer
+  auto body = [&](int s, auto copies) __attribute__((always_inline)) {
+    if constexpr (C::BK == 32) {
+      // The stages and waits of gemm_mainloop_direct_op.
+      phase(f0, f1, s, 1, 0, None());
+      if (s + 1 < nk) {
+        wait_stages<kPerStage, S - 3>(nk - 2 - s);
+        stage_barrier();
+      }
+      phase(f1, f0, s + 1, 0, s + kAhead, copies);
+    } else {
+      // Two stages of 64: once a stage's last fragments are in registers, its
+      // buffer takes the stage after the next, a step of 64 ahead of its use.
+      phase(f0, f1, s, 1, 0, None());
+      phase(f1, f0, s, 2, 0, None());
+      phase(f0, f1, s, 3, 0, None());
+      if (s + 1 < nk) {
+        __builtin_amdgcn_s_waitcnt(0x70);  // vmcnt and lgkmcnt 0: stage s + 1 is there, f1 is read
+        stage_barrier();
+      }
+      phase(f1, f0, s + 1, 0, s + kAhead, copies);
     }
-    read(f0, s + 1, 0);
-    asm volatile("" ::: "memory");
-    mma_frags<C>(acc, f1);
+  };
+#pragma unroll
+  for (int s = 0; s < (C::BK == 32 ? S - 1 : 2); ++s)
+    if (s < nk) issue_all(s);
+  wait_stages<kPerStage, (C::BK == 32 ? S - 2 : 1)>(nk - 1);
+  stage_barrier();
+  read_all(f0, 0, 0);
+  // Runs of stages that fill whole ones, and single ones that fill a tail or nothing.
+  const bool tails = p.K % C::BK != 0;
+  for (int s = 0; s < nk;) {
+    int end = nk - kAhead;
+    if (tails) {
+      const int tail = PAIR == kPairSum && first + s + kAhead < per ? per - 1 : total - 1;
+      if (tail - first - kAhead < end) end = tail - first - kAhead;
+    }
+    for (; s < end; ++s) body(s, Whole());
+    body(s, Any());
+    ++s;
   }
   __syncthreads();
   if constexpr (std::is_same<Epi, PartialEpilogue<Epi::kGated>>::value) epi.slice(at.slice);
