@@ -92,9 +92,9 @@ Cut cut_with(const Product& p, const TileSize& t, double& us) {
 }
 
 Cut cut_direct(const Product& p) {
-  const TileSize kTiles[] = {{kTileBig, 256, 256, p.kind == kProductTN ? 32 : 64, 4.4e12},
-                             {kTileMid, 128, 256, 32, 3.6e12},
-                             {kTileSmall, 128, 128, 32, 3.2e12}};
+  static const TileSize kTiles[] = {{kTileBig, 256, 256, 64, 4.9e12},
+                                    {kTileMid, 128, 256, 64, 3.6e12},
+                                    {kTileSmall, 128, 128, 64, 3.2e12}};
   Cut best = {};
   double least = 0;
   for (const TileSize& t : kTiles) {

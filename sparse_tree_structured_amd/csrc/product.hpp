@@ -23,11 +23,9 @@ struct Cut {
 Cut cut_product(const Product& p);
 
 template <typename E> using TileAny = AnyCfg<E, 128, 256, 64, 64>;
-template <ProductKind KIND>
-using TileBig = std::conditional_t<KIND == kProductTN, StepCfg<256, 256, 128, 64, 32, 4>,
-                                   StepCfg<256, 256, 128, 64, 64, 2>>;
-using TileMid = StepCfg<128, 256, 64, 64, 32, 4>;
-using TileSmall = StepCfg<128, 128, 64, 64, 32, 4>;  // two workgroups a compute unit
+using TileBig = StepCfg<256, 256, 128, 64, 2>;
+using TileMid = StepCfg<128, 256, 64, 64, 3>;
+using TileSmall = StepCfg<128, 128, 64, 64, 2>;  // two workgroups a compute unit
 
 template <class Epi>
 hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int N, const Epi& epi,
@@ -55,7 +53,7 @@ hipError_t launch_cut(const Product& p, const Epi& epi, const Cut& c, hipStream_
       return launch_tiles(product_direct_kernel<KIND, PAIR, C, Epi>, DirectParts<KIND, kTwo, C>::kLds,
                           C::kThreads, p, epi, c, st);
     };
-    if (c.tile == kTileBig) return direct(TileBig<KIND>());
+    if (c.tile == kTileBig) return direct(TileBig());
     if (c.tile == kTileMid) return direct(TileMid());
     if constexpr (!kTwo) {
       if (c.tile == kTileSmall) return direct(TileSmall());
