@@ -18,6 +18,7 @@
 
 #include "dense.hpp"
 #include "dense_any.hpp"
+#include "dense_epilogue.hpp"
 
 namespace fff {
 
@@ -61,6 +62,14 @@ __device__ __forceinline__ void each(const F& f) {
   }
 }
 
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const unsigned char* uniform(const unsigned char* p) {
+  const uintptr_t v = reinterpret_cast<uintptr_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const unsigned char*>(static_cast<uintptr_t>(hi) << 32 | lo);
+}
+
 // Where a lane's 16 bytes of 1 KB piece q of a stage's block of OUTER rows
 // (or columns) by BK of K come from: rows (or columns) outer, K from k on.
 template <int OUTER, int BK, Layout L>
@@ -98,7 +107,13 @@ struct DirectParts {
   using SB = Stager<uint16_t, kBCols, C::BK, kB, kBCols * C::BK / 8>;
   using PA = PieceAt<C::BM, C::BK, kA>;
   using PB = PieceAt<kBCols, C::BK, kB>;
-  static constexpr size_t kLds = C::kLdsBytes > band_bytes<C>() ? C::kLdsBytes : band_bytes<C>();
+  static constexpr size_t most(size_t a, size_t b) { return a > b ? a : b; }
+  static constexpr size_t out_bytes() {
+    if constexpr (PAIR) return most(GatedStage<C>::kBytes, band_bytes<C>());
+    return most(LinearStage<C>::kBytes, band_bytes<C>());
+  }
+  static constexpr size_t kLds = most(C::kLdsBytes, out_bytes());
+  static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
   static_assert(SA::kBytes == C::BM * C::BK * 2 && SB::kBytes == kBCols * C::BK * 2, "stage blocks");
 };
 
@@ -147,12 +162,12 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
     const int seg = PAIR == kPairSum && ks >= per ? 1 : 0;
     const int k = ks - seg * per;
     From f;
-    f.a = a0 + k * a_step + (PAIR == kPairSum ? seg * p.a_second * 2 : 0);
+    f.a = uniform(a0 + k * a_step + (PAIR == kPairSum ? seg * p.a_second * 2 : 0));
     const int64_t b = b0 + k * b_step;
     const bool second = PAIR == kPairSum ? seg != 0 : PAIR == kPairTwo && at.which != 0;
-    f.b0 = static_cast<const unsigned char*>(second ? p.b[1] : p.b[0]) + b;
-    f.b1 = kTwo ? static_cast<const unsigned char*>(p.b[1]) + b : nullptr;
-    f.to = lds_at + (s % S) * C::kStageBytes;
+    f.b0 = uniform(static_cast<const unsigned char*>(second ? p.b[1] : p.b[0]) + b);
+    f.b1 = kTwo ? uniform(static_cast<const unsigned char*>(p.b[1]) + b) : nullptr;
+    f.to = __builtin_amdgcn_readfirstlane(lds_at + (s % S) * C::kStageBytes);
     f.k_left = static_cast<int>(p.K) - k * C::BK;
     return f;
   };
@@ -267,8 +282,17 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
     ++s;
   }
   __syncthreads();
-  if constexpr (std::is_same<Epi, PartialEpilogue<Epi::kGated>>::value) epi.slice(at.slice);
-  tile_epilogue<C>(acc, lds, epi, m0, p.M, n0, p.N, at.which);
+  if constexpr (std::is_same<Epi, GatedEpilogue<uint16_t>>::value) {
+    gated_epilogue<C>(acc, lds, epi.e, m0, n0);
+  } else if constexpr (std::is_same<Epi, LinearEpilogue<uint16_t, uint16_t>>::value) {
+    if (epi.e.save[0] || reinterpret_cast<uintptr_t>(epi.e.residual) % 16 != 0)
+      tile_epilogue<C>(acc, lds, epi, m0, p.M, n0, p.N, at.which);
+    else
+      linear_epilogue<C>(acc, lds, epi.e, m0, n0, at.which);
+  } else {
+    if constexpr (std::is_same<Epi, PartialEpilogue<Epi::kGated>>::value) epi.slice(at.slice);
+    tile_epilogue<C>(acc, lds, epi, m0, p.M, n0, p.N, at.which);
+  }
 }
 
 }  // namespace fff
