@@ -152,12 +152,17 @@ bool product_fits(const Product& p) {
 
 // For pointers of any alignment.
 size_t product_workspace(const Product& p) {
-  const size_t any = cut_bytes(p, cut_any(p));
+  size_t most = cut_bytes(p, cut_any(p));
   const size_t direct = direct_sizes(p) ? cut_bytes(p, cut_direct(p)) : 0;
-  return any > direct ? any : direct;
+  const size_t small = small_product(p) ? small_workspace(p) : 0;
+  if (direct > most) most = direct;
+  return small > most ? small : most;
 }
 
 hipError_t launch_product(const Product& p, void* workspace, hipStream_t st) {
+  // (a few rows' kernel has 64 columns of a row together: no groups of 128)
+  const bool wide = (p.e.scale[0] || p.e.scale[1]) && p.e.group == 128;
+  if (small_product(p) && !wide) return launch_small(p, workspace, st);
   if (p.kind == kProductNN) return run_nn(p, workspace, st);
   return p.kind == kProductNT ? run_nt(p, workspace, st) : run_tn(p, workspace, st);
 }

@@ -87,6 +87,11 @@ hipError_t run_linear(const Product& p, void* workspace, hipStream_t st) {
   return run_with<E, KIND, PAIR>(p, LinearEpilogue<E, float>{p.e}, workspace, st);
 }
 
+// Few rows (dense_small.hpp).
+bool small_product(const Product& p);
+size_t small_workspace(const Product& p);
+hipError_t launch_small(const Product& p, void* workspace, hipStream_t st);
+
 hipError_t run_nn(const Product& p, void* workspace, hipStream_t st);
 hipError_t run_nt(const Product& p, void* workspace, hipStream_t st);
 hipError_t run_tn(const Product& p, void* workspace, hipStream_t st);
