@@ -196,8 +196,10 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
   const bool own_da = gated || s.act != FFF_ACT_NONE;
   const void* da = own_da ? ws + l.da : b.dy;
   hipError_t e = hipSuccess;
-  if ((own_da && products && s.T > 0) || (b.h && s.T > 0) || b.dbias) {
+  const bool restored = b.dW[0] && s.x_dtype == FFF_DTYPE_E4M3 && s.T > 0;
+  if ((own_da && products && s.T > 0) || (b.h && s.T > 0) || b.dbias || restored) {
     fff::ActBackward a = {};
+    if (restored) a.x = {s.T, s.K, s.x_group, b.x, b.x_scale, ws + l.x};
     a.T = s.T;
     a.N = s.N;
     a.bf16 = s.dtype == FFF_DTYPE_BF16;
@@ -229,15 +231,8 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
     if (e != hipSuccess) return FFF_ERROR_HIP;
   }
   if (b.dW[0]) {
-    const void* x = b.x;
-    if (s.x_dtype == FFF_DTYPE_E4M3 && s.T > 0) {
-      x = ws + l.x;
-      e = fff::launch_checkpoint_load(s.T, s.K, s.dtype == FFF_DTYPE_BF16, s.x_group, b.x, b.x_scale,
-                                      ws + l.x, stream);
-      if (e != hipSuccess) return FFF_ERROR_HIP;
-    }
     Product p = dw_product(s, gated);
-    p.a = x;
+    p.a = restored ? ws + l.x : b.x;
     p.b[0] = da;
     p.b[1] = static_cast<const unsigned char*>(da) + half;
     p.e.out[0] = b.dW[0];

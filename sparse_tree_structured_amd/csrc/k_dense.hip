@@ -65,7 +65,7 @@ double time_of(const Product& p, const TileSize& t, int64_t tiles, int64_t total
   double us = rounds * (steps * (step > 0.25 ? step : 0.25) + 4.0);
   if (slices > 1) {
     const int products = p.pair == kPairColumns || p.pair == kPairTwo ? 2 : 1;
-    us += 3.0 + 8.0 * slices * products * p.M * p.N / 4e6;
+    us += 5.0 + 8.0 * slices * products * p.M * p.N / 4e6;
   }
   return us;
 }

@@ -36,6 +36,33 @@ __device__ __forceinline__ void load_saved(float (&v)[V], const void* save, cons
   }
 }
 
+// Workgroup `block` of `blocks` that read a checkpoint: a wavefront has an
+// access of 64 lanes at a time.
+template <typename E>
+__device__ __forceinline__ void restore_rows(const Restore& r, int64_t block, int64_t blocks) {
+  constexpr int V = kLaneCols<E>;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int strips = (r.d + kWave * V - 1) / (kWave * V);
+  for (int64_t u = block * 4 + threadIdx.x / kWave; u < r.T * strips; u += blocks * 4) {
+    const size_t t = static_cast<size_t>(u / strips);
+    const int col = (static_cast<int>(u % strips) * kWave + lane) * V;
+    const int n = there(r.d - col, V);
+    float v[V];
+    load_saved<E>(v, r.codes, r.scale, r.group ? r.group : r.d, t, col, r.d, n);
+    if (n > 0) packed<E, V>(v).store(static_cast<E*>(r.x) + t * r.d + col, n);
+  }
+}
+
+int grid_of(int64_t units) {
+  const int64_t b = (units + 3) / 4;
+  return static_cast<int>(b < (1 << 20) ? b : (1 << 20));
+}
+
+int restore_grid(const Restore& r, bool bf16) {
+  const int cols = kWave * (bf16 ? 8 : 4);
+  return grid_of(r.T * ((int64_t(r.d) + cols - 1) / cols));
+}
+
 // Rows of one workgroup: four wavefronts take every fourth.
 constexpr int kStripRows = 64;
 constexpr int64_t kMaxStrips = 1024;  // of rows, where columns are summed
@@ -44,10 +71,16 @@ constexpr int64_t kMaxStrips = 1024;  // of rows, where columns are summed
 // act(gate), h = act(gate) up.  A workgroup has 64 lanes of columns and a
 // strip of rows; column sums are added over its rows in order, then over its
 // wavefronts, and one partial sum a strip is left for sum_strips_kernel.
+// The workgroups after those read x back.
 template <typename E, bool GATED>
 __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int col_blocks,
                                                            int64_t strips) {
   constexpr int V = kLaneCols<E>;
+  const int64_t act_blocks = col_blocks * strips;
+  if (blockIdx.x >= act_blocks) {
+    restore_rows<E>(a.x, blockIdx.x - act_blocks, gridDim.x - act_blocks);
+    return;
+  }
   __shared__ float sums[GATED ? 1 : 4][GATED ? 1 : kWave * V];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = threadIdx.x / kWave;
@@ -174,21 +207,8 @@ __global__ __launch_bounds__(256) void checkpoint_save_kernel(int64_t T, int d, 
 }
 
 template <typename E>
-__global__ __launch_bounds__(256) void checkpoint_load_kernel(int64_t T, int d, int group,
-                                                              const uint8_t* codes,
-                                                              const float* scale, E* x) {
-  constexpr int V = kLaneCols<E>;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int strips = (d + kWave * V - 1) / (kWave * V);
-  for (int64_t u = int64_t(blockIdx.x) * 4 + threadIdx.x / kWave; u < T * strips;
-       u += int64_t(gridDim.x) * 4) {
-    const size_t t = static_cast<size_t>(u / strips);
-    const int col = (static_cast<int>(u % strips) * kWave + lane) * V;
-    const int n = there(d - col, V);
-    float v[V];
-    load_saved<E>(v, codes, scale, group ? group : d, t, col, d, n);
-    if (n > 0) packed<E, V>(v).store(x + t * d + col, n);
-  }
+__global__ __launch_bounds__(256) void checkpoint_load_kernel(Restore r) {
+  restore_rows<E>(r, blockIdx.x, gridDim.x);
 }
 
 int64_t strips_of(int64_t T) {
@@ -197,27 +217,26 @@ int64_t strips_of(int64_t T) {
 }
 
 template <typename E, bool GATED>
-hipError_t run_act_backward(const ActBackward& a, hipStream_t st) {
+hipError_t run_act_backward(ActBackward a, hipStream_t st) {
   constexpr int kBlock = kWave * kLaneCols<E>;
   const int64_t col_blocks = (int64_t(a.N) + kBlock - 1) / kBlock;
-  const int64_t strips = strips_of(a.T);
-  if (strips > 0) {
-    act_backward_kernel<E, GATED><<<dim3(static_cast<uint32_t>(col_blocks * strips)), dim3(256), 0, st>>>(
+  // (nothing to do for dy's columns: x alone)
+  const int64_t strips = a.da || a.h || a.dbias ? strips_of(a.T) : 0;
+  const int64_t blocks = col_blocks * strips + (a.x.x ? restore_grid(a.x, sizeof(E) == 2) : 0);
+  const bool one_strip = strips == 1 && a.dbias;  // its sums are the result
+  if (one_strip) a.partial = a.dbias;
+  if (blocks > 0) {
+    act_backward_kernel<E, GATED><<<dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, st>>>(
         a, static_cast<int>(col_blocks), strips);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dbias) {
+  if (a.dbias && !one_strip) {
     sum_strips_kernel<<<dim3((a.N + 15) / 16), dim3(256), 0, st>>>(a.partial, static_cast<int>(strips),
                                                                    a.N, a.dbias);
     return hipGetLastError();
   }
   return hipSuccess;
-}
-
-int grid_of(int64_t units) {
-  const int64_t b = (units + 3) / 4;
-  return static_cast<int>(b < (1 << 20) ? b : (1 << 20));
 }
 
 }  // namespace
@@ -244,14 +263,12 @@ hipError_t launch_checkpoint_save(int64_t T, int d, bool bf16, int group, const 
 
 hipError_t launch_checkpoint_load(int64_t T, int d, bool bf16, int group, const void* codes,
                                   const float* scale, void* x, hipStream_t st) {
-  const uint8_t* q = static_cast<const uint8_t*>(codes);
-  const int cols = kWave * (bf16 ? 8 : 4);
-  const int grid = grid_of(T * ((int64_t(d) + cols - 1) / cols));
+  const Restore r = {T, d, group, codes, scale, x};
+  const int grid = restore_grid(r, bf16);
   if (bf16)
-    checkpoint_load_kernel<uint16_t><<<grid, 256, 0, st>>>(T, d, group, q, scale,
-                                                           static_cast<uint16_t*>(x));
+    checkpoint_load_kernel<uint16_t><<<grid, 256, 0, st>>>(r);
   else
-    checkpoint_load_kernel<float><<<grid, 256, 0, st>>>(T, d, group, q, scale, static_cast<float*>(x));
+    checkpoint_load_kernel<float><<<grid, 256, 0, st>>>(r);
   return hipGetLastError();
 }
 

@@ -60,7 +60,17 @@ bool product_fits(const Product& p);
 size_t product_workspace(const Product& p);
 hipError_t launch_product(const Product& p, void* workspace, hipStream_t st);
 
-// Elementwise part of the backward passes, and column sums.
+// An x kept in 8 bits, read back.
+struct Restore {
+  int64_t T;
+  int d, group;
+  const void* codes;
+  const float* scale;
+  void* x;  // null: none
+};
+
+// Elementwise part of the backward passes, column sums, and the x they need,
+// in one launch (and one more for the column sums' last step).
 struct ActBackward {
   int64_t T;
   int N;
@@ -75,6 +85,7 @@ struct ActBackward {
   void* h;                // gated: act(gate) * up [T,N], or null
   float* dbias;           // [N] sums over rows of da, or null
   float* partial;         // workspace of dbias
+  Restore x;
 };
 size_t act_backward_partials(int64_t T, int N, bool bf16);  // floats
 hipError_t launch_act_backward(const ActBackward& a, hipStream_t st);
