@@ -87,6 +87,31 @@ __device__ __forceinline__ void save_e4m3(const float (&v)[V], int n, uint8_t* c
     scales[static_cast<size_t>(row) * ((N + group - 1) / group) + col / group] = scale;
 }
 
+// V values into three planes, the first n of them stored; whether one is not
+// finite.  high is the nearest bf16 (towards zero where that would be
+// infinite), middle and low what is left, to nearest: high + middle + low is
+// the value where low is above bf16's smallest (values above 2^-110).
+template <int V>
+__device__ __forceinline__ bool store_planes(const float (&v)[V], uint16_t* at, int64_t plane, int n) {
+  float part[3][V];
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool finite = size_bits(v[i]) < 0x7f800000u;
+    odd |= !finite;
+    float h = bf16_to_f32(f32_to_bf16(v[i]));
+    if (size_bits(h) >= 0x7f800000u) h = __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+    const float r = v[i] - h;
+    const float m = bf16_to_f32(f32_to_bf16(r));
+    part[0][i] = h;
+    part[1][i] = m;
+    part[2][i] = r - m;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) packed<uint16_t, V>(part[k]).store(at + k * plane, n);
+  return odd;
+}
+
 // Epilogues.  apply() has four consecutive columns of a row, n (0 to 4) of
 // them there; lanes of 128 aligned columns come together, so that the groups
 // of 8-bit saves are complete.

@@ -128,6 +128,8 @@ __global__ __launch_bounds__(C::kThreads) void product_any_kernel(Product p, Epi
   constexpr bool kTwo = PAIR == kPairColumns;
   using P = AnyParts<E, KIND, kTwo, C>;
   extern __shared__ __align__(16) unsigned char lds[];
+  // (the product on planes has been made)
+  if (p.bad.word && *p.bad.word != p.bad.call) return;
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = tid / kWave;

@@ -117,14 +117,24 @@ struct DirectParts {
   static_assert(SA::kBytes == C::BM * C::BK * 2 && SB::kBytes == kBCols * C::BK * 2, "stage blocks");
 };
 
-template <ProductKind KIND, ProductPair PAIR, class C, class Epi>
+// SIX: the operands are the planes of float32 ones, h + m + l each, and K is
+// gone through six times: l h + h l + m m + m h + h m + h h, the small terms
+// first.  What is left out is about 2^-24 of the sizes' product, as one
+// rounding of a 32-bit product is; the matrix cores' bf16 rate is 16 times
+// their float32 rate, so this is worth 6 / 16 of it and the planes.
+constexpr uint32_t kSixA = 0x052;  // two bits a term: 2 0 1 1 0 0
+constexpr uint32_t kSixB = 0x118;  //                  0 2 1 0 1 0
+
+template <bool SIX, ProductKind KIND, ProductPair PAIR, class C, class Epi>
 __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, Epi epi, int tiles_m,
                                                                      int tiles_n, int steps) {
   constexpr bool kTwo = PAIR == kPairColumns;
   using P = DirectParts<KIND, kTwo, C>;
   constexpr int S = C::kStages;
   constexpr int kPerStage = C::kALoads + C::kBLoads;
+  constexpr int kTerms = SIX ? 6 : 1;
   extern __shared__ __align__(16) unsigned char lds[];
+  if (SIX && *p.bad.word == p.bad.call) return;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / C::kWavesN;
@@ -132,24 +142,33 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
   const TileAt at = tile_at(tiles_m, tiles_n, PAIR == kPairTwo ? 2 : 1);
   const int64_t m0 = int64_t(at.tm) * C::BM;
   const int n0 = at.tn * P::kBCols;
+  const int64_t lda = SIX ? p.a_planes.ld : p.lda;
+  const int64_t ldb = SIX ? p.b_planes[0].ld : p.ldb;
+  const int64_t a_second = SIX ? p.a_planes_second : p.a_second;
+  const void* const b_first = SIX ? p.b_planes[0].at : p.b[0];
+  const void* const b_other = SIX ? p.b_planes[1].at : p.b[1];
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane(
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)));
   uint32_t a_off[C::kALoads], b_off[C::kBLoads];
 #pragma unroll
   for (int j = 0; j < C::kALoads; ++j)
-    a_off[j] = typename P::PA(wave * C::kALoads + j, lane).offset(p.lda, p.M - m0);
+    a_off[j] = typename P::PA(wave * C::kALoads + j, lane).offset(lda, p.M - m0);
 #pragma unroll
   for (int j = 0; j < C::kBLoads; ++j)
-    b_off[j] = typename P::PB((wave * C::kBLoads + j) % P::kBPieces, lane).offset(p.ldb, p.N - n0);
-  const int64_t a_step = P::kA == kRows ? C::BK * 2 : p.lda * (C::BK * 2);  // bytes from a step to the next
-  const int64_t b_step = P::kB == kRows ? C::BK * 2 : p.ldb * (C::BK * 2);
+    b_off[j] = typename P::PB((wave * C::kBLoads + j) % P::kBPieces, lane).offset(ldb, p.N - n0);
+  const int64_t a_step = P::kA == kRows ? C::BK * 2 : lda * (C::BK * 2);  // bytes from a step to the next
+  const int64_t b_step = P::kB == kRows ? C::BK * 2 : ldb * (C::BK * 2);
   const unsigned char* a0 =
-      static_cast<const unsigned char*>(p.a) + 2 * (P::kA == kRows ? m0 * p.lda : m0);
-  const int64_t b0 = 2 * (P::kB == kRows ? int64_t(n0) * p.ldb : n0);
-  const int per = static_cast<int>((p.K + C::BK - 1) / C::BK);  // steps of one segment
-  const int total = PAIR == kPairSum ? 2 * per : per;
+      static_cast<const unsigned char*>(SIX ? p.a_planes.at : p.a) +
+      2 * (P::kA == kRows ? m0 * lda : m0);
+  const int64_t b0 = 2 * (P::kB == kRows ? int64_t(n0) * ldb : n0);
+  const int per = static_cast<int>((p.K + C::BK - 1) / C::BK);  // steps of one segment of K
+  const int total = per * kTerms * (PAIR == kPairSum ? 2 : 1);
   const int first = at.slice * steps;
   const int nk = (first + steps < total ? first + steps : total) - first;
+  // The segment and step that the next copied stage is of.
+  int next_seg = kTerms == 1 && PAIR != kPairSum ? 0 : first / (per > 0 ? per : 1);
+  int next_k = first - next_seg * per;
 
   // Where the copies of a stage come from and go to, the same for all lanes.
   struct From {
@@ -157,18 +176,29 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
     uint32_t to;
     int k_left;
   };
+  // (of stage s: asked for once for every stage, in their order)
   auto from = [&](int s) __attribute__((always_inline)) {
-    const int ks = first + s;
-    const int seg = PAIR == kPairSum && ks >= per ? 1 : 0;
-    const int k = ks - seg * per;
+    int64_t a_at = next_k * a_step, b_at = b0 + next_k * b_step;
+    bool second = PAIR == kPairTwo && at.which != 0;
+    if constexpr (SIX) {
+      const int term = PAIR == kPairSum && next_seg >= kTerms ? next_seg - kTerms : next_seg;
+      a_at += (kSixA >> (2 * term) & 3) * p.a_planes.plane * 2;
+      b_at += (kSixB >> (2 * term) & 3) * p.b_planes[0].plane * 2;
+    }
+    if (PAIR == kPairSum && next_seg >= kTerms) {
+      a_at += a_second * 2;
+      second = true;
+    }
     From f;
-    f.a = uniform(a0 + k * a_step + (PAIR == kPairSum ? seg * p.a_second * 2 : 0));
-    const int64_t b = b0 + k * b_step;
-    const bool second = PAIR == kPairSum ? seg != 0 : PAIR == kPairTwo && at.which != 0;
-    f.b0 = uniform(static_cast<const unsigned char*>(second ? p.b[1] : p.b[0]) + b);
-    f.b1 = kTwo ? uniform(static_cast<const unsigned char*>(p.b[1]) + b) : nullptr;
+    f.a = uniform(a0 + a_at);
+    f.b0 = uniform(static_cast<const unsigned char*>(second ? b_other : b_first) + b_at);
+    f.b1 = kTwo ? uniform(static_cast<const unsigned char*>(b_other) + b_at) : nullptr;
     f.to = __builtin_amdgcn_readfirstlane(lds_at + (s % S) * C::kStageBytes);
-    f.k_left = static_cast<int>(p.K) - k * C::BK;
+    f.k_left = static_cast<int>(p.K) - next_k * C::BK;
+    if (++next_k == per) {
+      next_k = 0;
+      ++next_seg;
+    }
     return f;
   };
   // Copy j (of kPerStage) of a wavefront; TAIL: the operands end in the stage.
@@ -232,7 +262,9 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
       __attribute__((always_inline)) {
     constexpr int kCopies = decltype(copies)::value;
     From stage;
-    if constexpr (kCopies != kNoCopies) stage = from(cs);
+    if constexpr (kCopies == kWholeCopies) stage = from(cs);
+    if constexpr (kCopies == kAnyCopies)
+      if (cs < nk) stage = from(cs);
     each<kMma>([&](auto m) __attribute__((always_inline)) {
       constexpr int i = m / C::kTn, j = m % C::kTn;
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
@@ -273,10 +305,7 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
   const bool tails = p.K % C::BK != 0;
   for (int s = 0; s < nk;) {
     int end = nk - S;
-    if (tails) {
-      const int tail = PAIR == kPairSum && first + s + S < per ? per - 1 : total - 1;
-      if (tail - first - S < end) end = tail - first - S;
-    }
+    if (tails && s + (per - 1 - next_k) < end) end = s + (per - 1 - next_k);
     for (; s < end; ++s) body(s, Whole());
     body(s, Any());
     ++s;

@@ -113,8 +113,22 @@ Product dw_product(const Shape& s, bool gated) {
 
 // The backward passes' workspace.
 struct Layout {
-  size_t da, x, strips, products, bytes;  // offsets, and all of it
+  size_t da, x, strips, planes, products, bytes;  // offsets, and all of it
 };
+
+// Whether da is needed in planes, too: float32 products large enough.
+bool split_da(const Shape& s, bool gated) {
+  return fff::split_wanted(dx_product(s, gated)) || fff::split_wanted(dw_product(s, gated));
+}
+
+// da's planes (gated: the gate's, then up's) from `at` on, in both products.
+void give_planes(const Shape& s, bool gated, unsigned char* at, Product& dx, Product& dw) {
+  if (!split_da(s, gated)) return;
+  const int64_t ld = fff::planes_ld(s.N), plane = s.T * ld;
+  dx.a_planes = dw.b_planes[0] = {at, ld, plane};
+  dx.a_planes_second = 3 * plane;
+  if (gated) dw.b_planes[1] = {at ? at + 6 * plane : nullptr, ld, plane};
+}
 
 Layout backward_layout(const Shape& s, bool gated) {
   const size_t e = type_size(s.dtype);
@@ -129,8 +143,12 @@ Layout backward_layout(const Shape& s, bool gated) {
   l.da = take(gated ? rows * s.N * 2 * e : s.act != FFF_ACT_NONE ? rows * s.N * e : 0);
   l.x = take(s.x_dtype == FFF_DTYPE_E4M3 ? rows * s.K * e : 0);
   l.strips = take(gated ? 0 : fff::act_backward_partials(s.T, s.N, s.dtype == FFF_DTYPE_BF16) * 4);
-  const size_t dx = fff::product_workspace(dx_product(s, gated));
-  const size_t dw = fff::product_workspace(dw_product(s, gated));
+  // (the word of values that are not finite, then the planes)
+  l.planes = take(split_da(s, gated) ? 256 + (gated ? 2 : 1) * fff::planes_bytes(s.T, s.N) : 0);
+  Product px = dx_product(s, gated), pw = dw_product(s, gated);
+  give_planes(s, gated, nullptr, px, pw);
+  const size_t dx = fff::product_workspace(px);
+  const size_t dw = fff::product_workspace(pw);
   l.products = take(dx > dw ? dx : dw);
   l.bytes = at;
   return l;
@@ -196,6 +214,16 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
   const bool own_da = gated || s.act != FFF_ACT_NONE;
   const void* da = own_da ? ws + l.da : b.dy;
   hipError_t e = hipSuccess;
+  Product px = dx_product(s, gated), pw = dw_product(s, gated);
+  const bool split = products && s.T > 0 && split_da(s, gated);
+  if (split) {
+    px.bad = pw.bad = {reinterpret_cast<unsigned long long*>(ws + l.planes), fff::call_number()};
+    give_planes(s, gated, ws + l.planes + 256, px, pw);
+    if (!own_da) {
+      e = fff::launch_split(b.dy, s.T, s.N, px.a_planes, px.bad, stream);
+      if (e != hipSuccess) return FFF_ERROR_HIP;
+    }
+  }
   const bool restored = b.dW[0] && s.x_dtype == FFF_DTYPE_E4M3 && s.T > 0;
   if ((own_da && products && s.T > 0) || (b.h && s.T > 0) || b.dbias || restored) {
     fff::ActBackward a = {};
@@ -213,6 +241,11 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
       }
       a.group = s.save_group ? s.save_group : s.N;
       a.da = products ? ws + l.da : nullptr;
+      if (split) {
+        a.da_planes[0] = pw.b_planes[0];
+        a.da_planes[1] = pw.b_planes[1];
+        a.bad = px.bad;
+      }
     }
     a.h = b.h;
     a.dbias = b.dbias;
@@ -222,22 +255,20 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
   }
   const size_t half = size_t(s.N) * type_size(s.dtype);
   if (b.dx && s.T > 0) {
-    Product p = dx_product(s, gated);
-    p.a = da;
-    p.b[0] = b.W[0];
-    p.b[1] = b.W[1];
-    p.e.out[0] = b.dx;
-    e = fff::launch_product(p, ws + l.products, stream);
+    px.a = da;
+    px.b[0] = b.W[0];
+    px.b[1] = b.W[1];
+    px.e.out[0] = b.dx;
+    e = fff::launch_product(px, ws + l.products, stream);
     if (e != hipSuccess) return FFF_ERROR_HIP;
   }
   if (b.dW[0]) {
-    Product p = dw_product(s, gated);
-    p.a = restored ? ws + l.x : b.x;
-    p.b[0] = da;
-    p.b[1] = static_cast<const unsigned char*>(da) + half;
-    p.e.out[0] = b.dW[0];
-    p.e.out[1] = b.dW[1];
-    e = fff::launch_product(p, ws + l.products, stream);
+    pw.a = restored ? ws + l.x : b.x;
+    pw.b[0] = da;
+    pw.b[1] = static_cast<const unsigned char*>(da) + half;
+    pw.e.out[0] = b.dW[0];
+    pw.e.out[1] = b.dW[1];
+    e = fff::launch_product(pw, ws + l.products, stream);
     if (e != hipSuccess) return FFF_ERROR_HIP;
   }
   return FFF_SUCCESS;

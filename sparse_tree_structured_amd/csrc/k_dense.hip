@@ -9,7 +9,9 @@ namespace {
 // has 256 columns of a row.
 template <class Epi>
 __global__ __launch_bounds__(256) void sum_slices_kernel(const float* partial, int slices,
-                                                         int products, int64_t M, int N, Epi epi) {
+                                                         int products, int64_t M, int N, Epi epi,
+                                                         NotFinite bad) {
+  if (bad.word && *bad.word == bad.call) return;
   const int lane = threadIdx.x & (kWave - 1);
   const int strips = (N + 255) / 256;
   const int64_t units = M * strips * (Epi::kGated ? 1 : products);
@@ -45,7 +47,7 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 // Whether the rows of both operands are whole 16-byte pieces.
 bool direct_sizes(const Product& p) {
-  if (!p.bf16 || p.lda % 8 != 0 || p.ldb % 8 != 0 || p.a_second % 8 != 0) return false;
+  if (p.lda % 8 != 0 || p.ldb % 8 != 0 || p.a_second % 8 != 0) return false;
   return p.kind == kProductTN || p.K % 8 == 0;
 }
 
@@ -78,7 +80,8 @@ Cut cut_with(const Product& p, const TileSize& t, double& us) {
   c.products = p.pair == kPairColumns || p.pair == kPairTwo ? 2 : 1;
   int64_t tiles = c.tiles_m * c.tiles_n * (p.pair == kPairTwo ? 2 : 1);
   if (tiles < 1) tiles = 1;
-  const int64_t total = ceil_div(p.K, t.bk) * (p.pair == kPairSum ? 2 : 1);
+  int64_t total = ceil_div(p.K, t.bk) * (p.pair == kPairSum ? 2 : 1);
+  if (!p.bf16 && t.tile != kTileAny) total *= 6;  // on planes
   int64_t slices = 1;
   us = time_of(p, t, tiles, total, 1);
   // Slices of at least four steps while tiles leave compute units idle.
@@ -111,6 +114,29 @@ Cut cut_any(const Product& p) {
   return cut_with(p, {kTileAny, 128, 256, p.bf16 ? 32 : 16, p.bf16 ? 3e12 : 0.4e12}, us);
 }
 
+// Splits of x [rows, cols] float32 into planes: a lane has eight columns, the
+// row's padding among them.
+__global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t rows, int64_t cols, Planes out,
+                                                    NotFinite bad) {
+  const int64_t pieces = out.ld / 8;
+  bool odd = false;
+  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < rows * pieces;
+       u += int64_t(gridDim.x) * 256) {
+    const int64_t row = u / pieces, col = u % pieces * 8;
+    float v[8];
+#pragma unroll
+    for (int h = 0; h < 8; h += 4) {
+      const int64_t left = cols - col - h;
+      Pack<float, 4> q;
+      q.load(x + row * cols + col + h, left < 4 ? static_cast<int>(left) : 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[h + i] = q.get(i);
+    }
+    odd |= store_planes<8>(v, static_cast<uint16_t*>(out.at) + row * out.ld + col, out.plane, 8);
+  }
+  if (odd) *bad.word = bad.call;
+}
+
 size_t cut_bytes(const Product& p, const Cut& c) {
   return c.slices <= 1 ? 0
                        : size_t(c.slices) * c.products * size_t(p.M) * size_t(p.N) * sizeof(float);
@@ -120,16 +146,16 @@ size_t cut_bytes(const Product& p, const Cut& c) {
 
 template <class Epi>
 hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int N, const Epi& epi,
-                             hipStream_t st) {
+                             const NotFinite& bad, hipStream_t st) {
   const int64_t units = M * ceil_div(N, 256) * (Epi::kGated ? 1 : c.products);
   const int64_t blocks = ceil_div(units, 4);
   sum_slices_kernel<Epi><<<dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
-                           st>>>(partial, c.slices, c.products, M, N, epi);
+                           st>>>(partial, c.slices, c.products, M, N, epi, bad);
   return hipGetLastError();
 }
 #define FFF_SUM(E)                                                                                \
   template hipError_t launch_sum_slices<E>(const float*, const Cut&, int64_t, int, const E&, \
-                                           hipStream_t)
+                                           const NotFinite&, hipStream_t)
 FFF_SUM(GatedEpilogue<uint16_t>);
 FFF_SUM(GatedEpilogue<float>);
 using LinearBf16 = LinearEpilogue<uint16_t, uint16_t>;
@@ -139,7 +165,35 @@ FFF_SUM(LinearBf16);
 FFF_SUM(LinearMixed);
 FFF_SUM(LinearF32);
 
+Cut cut_whole(const Product& p) {
+  Cut c = cut_any(p);
+  const int64_t total = ceil_div(p.K, p.bf16 ? 32 : 16) * (p.pair == kPairSum ? 2 : 1);
+  c.slices = 1;
+  c.steps = static_cast<int>(total);
+  return c;
+}
+
+// A product on planes takes six times the bf16 one's work at its rate, the
+// planes 10 bytes an element and two launches; on its values a sixteenth of
+// the rate.  8191 x 767 x 2045 takes 165 us instead of 240.
+bool split_wanted(const Product& p) {
+  if (p.bf16) return false;
+  const double pairs = p.pair == kSingle ? 1 : 2;
+  const double flops = 2.0 * pairs * p.M * p.N * p.K;
+  const double elements = double(p.M) * p.K * (p.pair == kPairSum ? 2 : 1) + pairs * p.K * p.N;
+  return flops / 90e6 > 6 * flops / 900e6 + 10 * elements / 4e6 + 25.0;
+}
+
+hipError_t launch_split(const void* x, int64_t rows, int64_t cols, const Planes& out,
+                        const NotFinite& bad, hipStream_t st) {
+  const int64_t blocks = ceil_div(rows * (out.ld / 8), 256);
+  split_kernel<<<dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st>>>(
+      static_cast<const float*>(x), rows, cols, out, bad);
+  return hipGetLastError();
+}
+
 Cut cut_product(const Product& p) {
+  if (!p.bf16) return p.bad.word ? cut_direct(p) : cut_any(p);
   const bool direct = direct_sizes(p) && aligned16(p.a) && aligned16(p.b[0]) && aligned16(p.b[1]);
   return direct ? cut_direct(p) : cut_any(p);
 }
@@ -150,19 +204,89 @@ bool product_fits(const Product& p) {
   return c.tiles_m * c.tiles_n * c.slices * 2 < (int64_t(1) << 22);
 }
 
+namespace {
+
+size_t padded(size_t bytes) { return (bytes + 255) & ~size_t(255); }
+
+// Rows and columns of an operand as it lies in memory.
+void a_sizes(const Product& p, int64_t& rows, int64_t& cols) {
+  rows = p.kind == kProductTN ? p.K : p.M;
+  cols = p.kind == kProductTN ? p.M : p.K;
+}
+void b_sizes(const Product& p, int64_t& rows, int64_t& cols) {
+  rows = p.kind == kProductNT ? p.N : p.K;
+  cols = p.kind == kProductNT ? p.K : p.N;
+}
+
+// Where a product on planes has what it makes: the slices' sums, a word, and
+// the planes of the operands that have none yet (no row length).
+struct PlanesAt {
+  size_t word, a, b[2], bytes;
+};
+PlanesAt planes_at(const Product& p) {
+  PlanesAt l = {};
+  int64_t rows, cols;
+  l.word = padded(cut_bytes(p, cut_direct(p)));
+  l.bytes = l.word + 256;
+  if (p.a_planes.ld == 0) {
+    a_sizes(p, rows, cols);
+    l.a = l.bytes;
+    l.bytes += padded(planes_bytes(rows, cols));
+  }
+  b_sizes(p, rows, cols);
+  for (int i = 0; i < (p.pair == kSingle ? 1 : 2); ++i)
+    if (p.b_planes[i].ld == 0) {
+      l.b[i] = l.bytes;
+      l.bytes += padded(planes_bytes(rows, cols));
+    }
+  return l;
+}
+
+hipError_t split_operand(const void* x, int64_t rows, int64_t cols, unsigned char* to, Planes& out,
+                         const NotFinite& bad, hipStream_t st) {
+  out = {to, planes_ld(cols), rows * planes_ld(cols)};
+  return launch_split(x, rows, cols, out, bad, st);
+}
+
+}  // namespace
+
 // For pointers of any alignment.
 size_t product_workspace(const Product& p) {
   size_t most = cut_bytes(p, cut_any(p));
-  const size_t direct = direct_sizes(p) ? cut_bytes(p, cut_direct(p)) : 0;
+  const size_t direct = p.bf16 ? (direct_sizes(p) ? cut_bytes(p, cut_direct(p)) : 0)
+                               : (split_wanted(p) ? planes_at(p).bytes : 0);
   const size_t small = small_product(p) ? small_workspace(p) : 0;
   if (direct > most) most = direct;
   return small > most ? small : most;
 }
 
-hipError_t launch_product(const Product& p, void* workspace, hipStream_t st) {
+hipError_t launch_product(const Product& product, void* workspace, hipStream_t st) {
+  Product p = product;
   // (a few rows' kernel has 64 columns of a row together: no groups of 128)
   const bool wide = (p.e.scale[0] || p.e.scale[1]) && p.e.group == 128;
-  if (small_product(p) && !wide) return launch_small(p, workspace, st);
+  if (small_product(p) && !wide) {
+    p.bad = {};
+    return launch_small(p, workspace, st);
+  }
+  if (!split_wanted(p)) {
+    p.bad = {};
+  } else {
+    unsigned char* const ws = static_cast<unsigned char*>(workspace);
+    const PlanesAt l = planes_at(p);
+    hipError_t e = hipSuccess;
+    int64_t rows, cols;
+    if (!p.bad.word)
+      p.bad = {reinterpret_cast<unsigned long long*>(ws + l.word), call_number()};
+    if (!p.a_planes.at) {
+      a_sizes(p, rows, cols);
+      e = split_operand(p.a, rows, cols, ws + l.a, p.a_planes, p.bad, st);
+    }
+    b_sizes(p, rows, cols);
+    for (int i = 0; i < (p.pair == kSingle ? 1 : 2); ++i)
+      if (e == hipSuccess && !p.b_planes[i].at)
+        e = split_operand(p.b[i], rows, cols, ws + l.b[i], p.b_planes[i], p.bad, st);
+    if (e != hipSuccess) return e;
+  }
   if (p.kind == kProductNN) return run_nn(p, workspace, st);
   return p.kind == kProductNT ? run_nt(p, workspace, st) : run_tn(p, workspace, st);
 }

@@ -88,6 +88,15 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
   const int col = (blockIdx.x % col_blocks * kWave + lane) * V;
   const int n = there(a.N - col, V);
   float total[V] = {};
+  bool odd = false;
+  // (with planes a row's padding is zeros in them)
+  const int n_plane = a.da_planes[0].at ? there(a.da_planes[0].ld - col, V) : 0;
+  auto planes = [&](int which, const float (&v)[V], size_t row) {
+    if constexpr (sizeof(E) == 4)
+      if (n_plane > 0)
+        odd |= store_planes<V>(v, static_cast<uint16_t*>(a.da_planes[which].at) +
+                                      row * a.da_planes[0].ld + col, a.da_planes[0].plane, n_plane);
+  };
   for (int64_t r0 = strip * kStripRows; r0 < a.T; r0 += strips * kStripRows) {
     const int64_t end = r0 + kStripRows < a.T ? r0 + kStripRows : a.T;
     for (int64_t t = r0 + wave; t < end; t += 4) {
@@ -107,6 +116,8 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
           du[i] = dy.get(i) * value;
           h[i] = value * up[i];
         }
+        planes(0, da, row);
+        planes(1, du, row);
         if (n > 0) {
           if (a.da) {
             E* out = static_cast<E*>(a.da) + row * (2 * size_t(a.N)) + col;
@@ -126,10 +137,12 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
           }
           total[i] += da[i];
         }
+        planes(0, da, row);
         if (a.da && n > 0) packed<E, V>(da).store(static_cast<E*>(a.da) + row * a.N + col, n);
       }
     }
   }
+  if (odd) *a.bad.word = a.bad.call;
   if constexpr (!GATED) {
     if (!a.partial) return;
 #pragma unroll

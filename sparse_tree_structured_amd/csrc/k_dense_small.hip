@@ -26,16 +26,6 @@ int64_t word_floats(int64_t blocks, int64_t slices) { return (blocks * (slices +
 
 int row_tiles(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
-// Numbers that no other call has.
-unsigned long long call_number() {
-  static std::atomic<unsigned long long> next{
-      static_cast<unsigned long long>(
-          std::chrono::system_clock::now().time_since_epoch().count()) *
-      0x9E3779B97F4A7C15ull};
-  const unsigned long long n = next.fetch_add(1);
-  return n ? n : next.fetch_add(1);
-}
-
 template <typename E, int TT, class Epi>
 hipError_t launch(const Product& p, const Epi& epi, void* workspace, hipStream_t st) {
   const int64_t blocks = col_blocks(p);
@@ -86,6 +76,15 @@ hipError_t run_type(const Product& p, void* workspace, hipStream_t st) {
 }
 
 }  // namespace
+
+unsigned long long call_number() {
+  static std::atomic<unsigned long long> next{
+      static_cast<unsigned long long>(
+          std::chrono::system_clock::now().time_since_epoch().count()) *
+      0x9E3779B97F4A7C15ull};
+  const unsigned long long n = next.fetch_add(1);
+  return n ? n : next.fetch_add(1);
+}
 
 bool small_product(const Product& p) {
   return p.kind == kProductNN && p.M <= kSmallRows && p.K < (int64_t(1) << 31) - kSmallStep;

@@ -40,6 +40,26 @@ struct Epilogue {
   int group;            // columns of a scale
 };
 
+// A float32 matrix as three bf16 planes, the value being their sum: high
+// (nearest), middle (the rest's nearest) and low.  Rows are padded with zeros
+// to whole 16-byte pieces.
+struct Planes {
+  void* at;       // null: none
+  int64_t ld;     // elements from a row to the next
+  int64_t plane;  // elements from a plane to the next
+};
+inline int64_t planes_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
+inline size_t planes_bytes(int64_t rows, int64_t cols) {
+  return 3 * size_t(rows) * size_t(planes_ld(cols)) * 2;
+}
+
+// A word that holds the call's number once a value that is not finite was met.
+struct NotFinite {
+  unsigned long long* word;  // null: not asked
+  unsigned long long call;
+};
+unsigned long long call_number();  // one that no other call has
+
 struct Product {
   ProductKind kind;
   ProductPair pair;
@@ -52,7 +72,19 @@ struct Product {
   int N;
   int64_t K;      // of one product
   Epilogue e;
+  // float32 operands in planes (split_wanted), and whether all are finite: the
+  // kernel on planes runs if they are, the other one if not.  at of both
+  // pairs' planes; the second A's follow the first's a_planes_second later.
+  Planes a_planes, b_planes[2];
+  int64_t a_planes_second;
+  NotFinite bad;
 };
+
+// Whether a float32 product is worth its operands' split into planes.
+bool split_wanted(const Product& p);
+// x [rows, cols] float32 into planes.
+hipError_t launch_split(const void* x, int64_t rows, int64_t cols, const Planes& out,
+                        const NotFinite& bad, hipStream_t st);
 
 // Whether its tiles fit one launch.
 bool product_fits(const Product& p);
@@ -85,6 +117,8 @@ struct ActBackward {
   void* h;                // gated: act(gate) * up [T,N], or null
   float* dbias;           // [N] sums over rows of da, or null
   float* partial;         // workspace of dbias
+  Planes da_planes[2];    // float32: da (gated: the gate's and up's) once more in planes, or none
+  NotFinite bad;
   Restore x;
 };
 size_t act_backward_partials(int64_t T, int N, bool bf16);  // floats

@@ -21,15 +21,18 @@ struct Cut {
   int slices, steps;  // of K
 };
 Cut cut_product(const Product& p);
+// In tiles of any sizes, K in one piece.
+Cut cut_whole(const Product& p);
 
 template <typename E> using TileAny = AnyCfg<E, 128, 256, 64, 64>;
 using TileBig = StepCfg<256, 256, 128, 64, 2>;
 using TileMid = StepCfg<128, 256, 64, 64, 3>;
 using TileSmall = StepCfg<128, 128, 64, 64, 2>;  // two workgroups a compute unit
 
+// The slices' sums through the epilogue (nothing where `bad` holds the call's number).
 template <class Epi>
 hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int N, const Epi& epi,
-                             hipStream_t st);
+                             const NotFinite& bad, hipStream_t st);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -44,22 +47,31 @@ hipError_t launch_tiles(Kernel kern, size_t lds, int threads, const Product& p, 
   return hipGetLastError();
 }
 
+// In tiles straight into LDS: bf16 operands, or (SIX) float32 ones' planes.
+template <bool SIX, ProductKind KIND, ProductPair PAIR, class Epi>
+hipError_t launch_direct(const Product& p, const Epi& epi, const Cut& c, hipStream_t st) {
+  constexpr bool kTwo = PAIR == kPairColumns;
+  auto direct = [&](auto cfg) {
+    using C = decltype(cfg);
+    return launch_tiles(product_direct_kernel<SIX, KIND, PAIR, C, Epi>,
+                        DirectParts<KIND, kTwo, C>::kLds, C::kThreads, p, epi, c, st);
+  };
+  if (c.tile == kTileBig) return direct(TileBig());
+  if constexpr (!kTwo) {
+    if (c.tile == kTileSmall) return direct(TileSmall());
+  }
+  return direct(TileMid());
+}
+
 template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
 hipError_t launch_cut(const Product& p, const Epi& epi, const Cut& c, hipStream_t st) {
-  constexpr bool kTwo = PAIR == kPairColumns;
   if constexpr (sizeof(E) == 2) {
-    auto direct = [&](auto cfg) {
-      using C = decltype(cfg);
-      return launch_tiles(product_direct_kernel<KIND, PAIR, C, Epi>, DirectParts<KIND, kTwo, C>::kLds,
-                          C::kThreads, p, epi, c, st);
-    };
-    if (c.tile == kTileBig) return direct(TileBig());
-    if (c.tile == kTileMid) return direct(TileMid());
-    if constexpr (!kTwo) {
-      if (c.tile == kTileSmall) return direct(TileSmall());
-    }
+    if (c.tile != kTileAny) return launch_direct<false, KIND, PAIR>(p, epi, c, st);
+  } else {
+    if (c.tile != kTileAny) return launch_direct<true, KIND, PAIR>(p, epi, c, st);
   }
   using C = TileAny<E>;
+  constexpr bool kTwo = PAIR == kPairColumns;
   return launch_tiles(product_any_kernel<E, KIND, PAIR, C, Epi>, AnyParts<E, KIND, kTwo, C>::kLds,
                       C::kThreads, p, epi, c, st);
 }
@@ -67,15 +79,22 @@ hipError_t launch_cut(const Product& p, const Epi& epi, const Cut& c, hipStream_
 template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
 hipError_t run_with(const Product& p, const Epi& epi, void* workspace, hipStream_t st) {
   const Cut c = cut_product(p);
-  if (c.slices <= 1) return launch_cut<E, KIND, PAIR>(p, epi, c, st);
-  PartialEpilogue<Epi::kGated> part;
-  part.partial = static_cast<float*>(workspace);
-  part.M = p.M;
-  part.N = p.N;
-  part.products = c.products;
-  const hipError_t e = launch_cut<E, KIND, PAIR>(p, part, c, st);
-  if (e != hipSuccess) return e;
-  return launch_sum_slices(part.partial, c, p.M, p.N, epi, st);
+  hipError_t e;
+  if (c.slices <= 1) {
+    e = launch_cut<E, KIND, PAIR>(p, epi, c, st);
+  } else {
+    PartialEpilogue<Epi::kGated> part;
+    part.partial = static_cast<float*>(workspace);
+    part.M = p.M;
+    part.N = p.N;
+    part.products = c.products;
+    e = launch_cut<E, KIND, PAIR>(p, part, c, st);
+    if (e == hipSuccess) e = launch_sum_slices(part.partial, c, p.M, p.N, epi, p.bad, st);
+  }
+  // On planes: the kernel on the values themselves, should they not be finite.
+  if (e == hipSuccess && p.bad.word)
+    e = launch_cut<E, KIND, PAIR>(p, epi, cut_whole(p), st);
+  return e;
 }
 
 // Out and residual in the layer's type or in 32 bits.
