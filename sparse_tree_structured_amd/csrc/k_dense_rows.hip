@@ -15,26 +15,35 @@ __host__ __device__ constexpr int there(int64_t left, int most) {
   return left < 0 ? 0 : left < most ? static_cast<int>(left) : most;
 }
 
-// A value kept for the backward pass, in the layer's type or in 8 bits.
+// V values kept for the backward pass, in the layer's type or in 8 bits.
 template <typename E, int V>
-__device__ __forceinline__ void load_saved(float (&v)[V], const void* save, const float* scale,
-                                           int group, size_t row, int col, int N, int n) {
-  if (scale) {
-    Pack<uint8_t, V> q;
-    q.load(static_cast<const uint8_t*>(save) + row * N + col, n);
-    unpack_e4m3(q, v);
-    if (n <= 0) return;
-    // V divides the group, and col is a multiple of V: one scale a lane
-    const float s = scale[row * ((N + group - 1) / group) + col / group];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= s;
-  } else {
-    Pack<E, V> q;
-    q.load(static_cast<const E*>(save) + row * N + col, n);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = q.get(i);
+struct Saved {
+  Pack<E, V> same;
+  Pack<uint8_t, V> codes;
+  float scale;
+
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const void* save, const float* scales, int group, size_t row,
+                                       int col, int N, int n) {
+    if (scales) {
+      codes.template load<STREAM>(static_cast<const uint8_t*>(save) + row * N + col, n);
+      // V divides the group, and col is a multiple of V: one scale a lane
+      scale = n > 0 ? scales[row * ((N + group - 1) / group) + col / group] : 0.0f;
+    } else {
+      same.template load<STREAM>(static_cast<const E*>(save) + row * N + col, n);
+    }
   }
-}
+  __device__ __forceinline__ void get(float (&v)[V], bool eight) const {
+    if (eight) {
+      unpack_e4m3(codes, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = same.get(i);
+    }
+  }
+};
 
 // Workgroup `block` of `blocks` that read a checkpoint: a wavefront has an
 // access of 64 lanes at a time.
@@ -47,8 +56,10 @@ __device__ __forceinline__ void restore_rows(const Restore& r, int64_t block, in
     const size_t t = static_cast<size_t>(u / strips);
     const int col = (static_cast<int>(u % strips) * kWave + lane) * V;
     const int n = there(r.d - col, V);
+    Saved<E, V> q;
+    q.template load<false>(r.codes, r.scale, r.group ? r.group : r.d, t, col, r.d, n);
     float v[V];
-    load_saved<E>(v, r.codes, r.scale, r.group ? r.group : r.d, t, col, r.d, n);
+    q.get(v, true);
     if (n > 0) packed<E, V>(v).store(static_cast<E*>(r.x) + t * r.d + col, n);
   }
 }
@@ -63,18 +74,23 @@ int restore_grid(const Restore& r, bool bf16) {
   return grid_of(r.T * ((int64_t(r.d) + cols - 1) / cols));
 }
 
-// Rows of one workgroup: four wavefronts take every fourth.
-constexpr int kStripRows = 64;
-constexpr int64_t kMaxStrips = 1024;  // of rows, where columns are summed
+// Rows of a strip: 64 (four wavefronts take every fourth), or fewer where that
+// leaves compute units without work: 512 x 1024 in bf16 takes 4 us with 4
+// rows and 20 with 64, most of it one row's load after the other.
+int strip_rows(int64_t T, int64_t col_blocks) {
+  const int64_t r = T * col_blocks / 1024 / 4 * 4;
+  return r < 4 ? 4 : r < 64 ? static_cast<int>(r) : 64;
+}
+constexpr int64_t kMaxStrips = 1024;  // a workgroup takes more than one, then
 
 // da = dy act'(pre); of the gated pair dgate = dh up act'(gate) and dup = dh
 // act(gate), h = act(gate) up.  A workgroup has 64 lanes of columns and a
 // strip of rows; column sums are added over its rows in order, then over its
 // wavefronts, and one partial sum a strip is left for sum_strips_kernel.
 // The workgroups after those read x back.
-template <typename E, bool GATED>
+template <typename E, bool GATED, int ACT>
 __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int col_blocks,
-                                                           int64_t strips) {
+                                                           int64_t strips, int strip) {
   constexpr int V = kLaneCols<E>;
   const int64_t act_blocks = col_blocks * strips;
   if (blockIdx.x >= act_blocks) {
@@ -84,7 +100,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
   __shared__ float sums[GATED ? 1 : 4][GATED ? 1 : kWave * V];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = threadIdx.x / kWave;
-  const int64_t strip = blockIdx.x / col_blocks;
+  const int64_t first = blockIdx.x / col_blocks;
   const int col = (blockIdx.x % col_blocks * kWave + lane) * V;
   const int n = there(a.N - col, V);
   float total[V] = {};
@@ -97,24 +113,27 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
         odd |= store_planes<V>(v, static_cast<uint16_t*>(a.da_planes[which].at) +
                                       row * a.da_planes[0].ld + col, a.da_planes[0].plane, n_plane);
   };
-  for (int64_t r0 = strip * kStripRows; r0 < a.T; r0 += strips * kStripRows) {
-    const int64_t end = r0 + kStripRows < a.T ? r0 + kStripRows : a.T;
+  for (int64_t r0 = first * strip; r0 < a.T; r0 += strips * strip) {
+    const int64_t end = r0 + strip < a.T ? r0 + strip : a.T;
     for (int64_t t = r0 + wave; t < end; t += 4) {
       const size_t row = static_cast<size_t>(t);
       Pack<E, V> dy;
-      dy.load(static_cast<const E*>(a.dy) + row * a.N + col, n);
-      float pre[V], up[V], da[V];
-      if (a.save[0]) load_saved<E>(pre, a.save[0], a.scale[0], a.group, row, col, a.N, n);
+      Saved<E, V> pre, up;
+      dy.template load<GATED>(static_cast<const E*>(a.dy) + row * a.N + col, n);
+      if (a.save[0]) pre.template load<GATED>(a.save[0], a.scale[0], a.group, row, col, a.N, n);
+      if constexpr (GATED) up.template load<true>(a.save[1], a.scale[1], a.group, row, col, a.N, n);
+      float p[V], da[V];
+      if (a.save[0]) pre.get(p, a.scale[0] != nullptr);
       if constexpr (GATED) {
-        load_saved<E>(up, a.save[1], a.scale[1], a.group, row, col, a.N, n);
-        float du[V], h[V];
+        float w[V], du[V], h[V];
+        up.get(w, a.scale[1] != nullptr);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           float value, slope;
-          activation_slope(pre[i], a.act, value, slope);
-          da[i] = dy.get(i) * up[i] * slope;
+          activation_slope(p[i], ACT, value, slope);
+          da[i] = dy.get(i) * w[i] * slope;
           du[i] = dy.get(i) * value;
-          h[i] = value * up[i];
+          h[i] = value * w[i];
         }
         planes(0, da, row);
         planes(1, du, row);
@@ -124,7 +143,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
             packed<E, V>(da).store(out, n);
             packed<E, V>(du).store(out + a.N, n);
           }
-          if (a.h) packed<E, V>(h).store(static_cast<E*>(a.h) + row * a.N + col, n);
+          if (a.h) packed<E, V>(h).template store<true>(static_cast<E*>(a.h) + row * a.N + col, n);
         }
       } else {
 #pragma unroll
@@ -132,7 +151,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
           da[i] = dy.get(i);
           if (a.save[0]) {
             float value, slope;
-            activation_slope(pre[i], a.act, value, slope);
+            activation_slope(p[i], ACT, value, slope);
             da[i] *= slope;
           }
           total[i] += da[i];
@@ -151,7 +170,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
     for (int c = threadIdx.x; c < kWave * V; c += 256) {
       const int at = blockIdx.x % col_blocks * kWave * V + c;
       if (at < a.N)
-        a.partial[static_cast<size_t>(strip) * a.N + at] =
+        a.partial[static_cast<size_t>(first) * a.N + at] =
             (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
     }
   }
@@ -224,23 +243,38 @@ __global__ __launch_bounds__(256) void checkpoint_load_kernel(Restore r) {
   restore_rows<E>(r, blockIdx.x, gridDim.x);
 }
 
-int64_t strips_of(int64_t T) {
-  const int64_t s = (T + kStripRows - 1) / kStripRows;
+int64_t col_blocks_of(int N, bool bf16) {
+  const int cols = kWave * (bf16 ? 8 : 4);
+  return (int64_t(N) + cols - 1) / cols;
+}
+
+int64_t strips_of(int64_t T, int N, bool bf16) {
+  const int r = strip_rows(T, col_blocks_of(N, bf16));
+  const int64_t s = (T + r - 1) / r;
   return s < kMaxStrips ? s : kMaxStrips;
 }
 
 template <typename E, bool GATED>
 hipError_t run_act_backward(ActBackward a, hipStream_t st) {
-  constexpr int kBlock = kWave * kLaneCols<E>;
-  const int64_t col_blocks = (int64_t(a.N) + kBlock - 1) / kBlock;
+  constexpr bool kBf16 = sizeof(E) == 2;
+  const int64_t col_blocks = col_blocks_of(a.N, kBf16);
   // (nothing to do for dy's columns: x alone)
-  const int64_t strips = a.da || a.h || a.dbias ? strips_of(a.T) : 0;
-  const int64_t blocks = col_blocks * strips + (a.x.x ? restore_grid(a.x, sizeof(E) == 2) : 0);
+  const int64_t strips = a.da || a.h || a.dbias ? strips_of(a.T, a.N, kBf16) : 0;
+  const int64_t blocks = col_blocks * strips + (a.x.x ? restore_grid(a.x, kBf16) : 0);
   const bool one_strip = strips == 1 && a.dbias;  // its sums are the result
   if (one_strip) a.partial = a.dbias;
   if (blocks > 0) {
-    act_backward_kernel<E, GATED><<<dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, st>>>(
-        a, static_cast<int>(col_blocks), strips);
+    auto launch = [&](auto act) {
+      act_backward_kernel<E, GATED, decltype(act)::value>
+          <<<dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, st>>>(
+              a, static_cast<int>(col_blocks), strips, strip_rows(a.T, col_blocks));
+    };
+    switch (a.act) {
+      case kActGelu: launch(std::integral_constant<int, kActGelu>()); break;
+      case kActSilu: launch(std::integral_constant<int, kActSilu>()); break;
+      case kActRelu: launch(std::integral_constant<int, kActRelu>()); break;
+      default: launch(std::integral_constant<int, kActNone>());
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -254,7 +288,9 @@ hipError_t run_act_backward(ActBackward a, hipStream_t st) {
 
 }  // namespace
 
-size_t act_backward_partials(int64_t T, int N, bool) { return size_t(strips_of(T)) * size_t(N); }
+size_t act_backward_partials(int64_t T, int N, bool bf16) {
+  return size_t(strips_of(T, N, bf16)) * size_t(N);
+}
 
 hipError_t launch_act_backward(const ActBackward& a, hipStream_t st) {
   if (a.gated)
