@@ -5,15 +5,13 @@
 // follow one another along K, and K ends anywhere: in the last step the
 // pieces past it come from 16 zero bytes.
 //
-// A step is 64 of K (a K-contiguous row's piece is a whole 128-byte line), in
-// two or three LDS stages.  Once a stage's last fragments are in registers,
-// its buffer takes the stage that far ahead.  Copies and fragment reads are
-// issued one by one between matrix-core operations, and a copy is one
-// instruction with a uniform base, made once a stage, and 32 bits of offset
-// for each lane that stay the same over the loop: with the copies in one
-// piece and their addresses made for each, the matrix cores had work in 57 %
-// of the cycles (16384 x 8192 x 8192 2030 us), so they have it in 70 %
-// (1750 us).
+// A step is 64 of K (a K-contiguous row's piece is a whole 128-byte line).
+// Once a stage's last fragments are in registers, its buffers take the stages
+// as far ahead as there are buffers.  Copies and fragment reads are issued one
+// by one between matrix-core operations, and a copy is one instruction with a
+// uniform base, made once a stage, and 32 bits of offset for each lane that
+// stay the same over the loop: with the copies in one piece and their
+// addresses made for each, the matrix cores had work in 57 % of the cycles.
 #pragma once
 
 #include "dense.hpp"
@@ -38,16 +36,18 @@ __device__ __forceinline__ void dma16_base(const void* base, uint32_t offset, ui
       : "memory");
 }
 
-// Tiles of BM x BN, a wavefront WM x WN of them, in STAGES stages.
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+// Tiles of BM x BN, a wavefront WM x WN of them, with A_STAGES buffers of A and
+// one fewer of B.
+template <int BM_, int BN_, int WM_, int WN_, int A_STAGES>
 struct StepCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = 64;
-  static constexpr int kStages = STAGES_;
+  static constexpr int kAStages = A_STAGES, kBStages = A_STAGES - 1;
+  static_assert(kBStages >= 2, "a stage is filled while another is used");
   static constexpr int kWavesM = BM / WM, kWavesN = BN / WN, kWaves = kWavesM * kWavesN;
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int kTm = WM / 32, kTn = WN / 32;
-  static constexpr int kStageBytes = (BM + BN) * BK * 2;
-  static constexpr size_t kLdsBytes = size_t(kStages) * kStageBytes;
+  static constexpr int kABytes = BM * BK * 2, kBBytes = BN * BK * 2;  // of a stage
+  static constexpr size_t kLdsBytes = size_t(kAStages) * kABytes + size_t(kBStages) * kBBytes;
   static constexpr int kALoads = BM * BK / 512 / kWaves;  // 1 KB copies of a wavefront and stage
   static constexpr int kBLoads = BN * BK / 512 / kWaves;
   static_assert(BM * BK % (512 * kWaves) == 0 && BN * BK % (512 * kWaves) == 0, "whole copies");
@@ -130,8 +130,7 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
                                                                      int tiles_n, int steps) {
   constexpr bool kTwo = PAIR == kPairColumns;
   using P = DirectParts<KIND, kTwo, C>;
-  constexpr int S = C::kStages;
-  constexpr int kPerStage = C::kALoads + C::kBLoads;
+  constexpr int kACopies = C::kALoads, kBCopies = C::kBLoads;
   constexpr int kTerms = SIX ? 6 : 1;
   extern __shared__ __align__(16) unsigned char lds[];
   if (SIX && *p.bad.word == p.bad.call) return;
@@ -166,75 +165,88 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
   const int total = per * kTerms * (PAIR == kPairSum ? 2 : 1);
   const int first = at.slice * steps;
   const int nk = (first + steps < total ? first + steps : total) - first;
-  // The segment and step that the next copied stage is of.
-  int next_seg = kTerms == 1 && PAIR != kPairSum ? 0 : first / (per > 0 ? per : 1);
-  int next_k = first - next_seg * per;
 
-  // Where the copies of a stage come from and go to, the same for all lanes.
+  // Where the copies of an operand's next stage come from and go to, the same
+  // for all lanes: asked for once for every stage, in their order.
   struct From {
-    const unsigned char *a, *b0, *b1;
+    const unsigned char *p0, *p1;
     uint32_t to;
     int k_left;
   };
-  // (of stage s: asked for once for every stage, in their order)
-  auto from = [&](int s) __attribute__((always_inline)) {
-    int64_t a_at = next_k * a_step, b_at = b0 + next_k * b_step;
-    bool second = PAIR == kPairTwo && at.which != 0;
-    if constexpr (SIX) {
-      const int term = PAIR == kPairSum && next_seg >= kTerms ? next_seg - kTerms : next_seg;
-      a_at += (kSixA >> (2 * term) & 3) * p.a_planes.plane * 2;
-      b_at += (kSixB >> (2 * term) & 3) * p.b_planes[0].plane * 2;
+  struct Next {
+    int seg, k;  // segment of K and step in it
+  };
+  const int seg0 = kTerms == 1 && PAIR != kPairSum ? 0 : first / (per > 0 ? per : 1);
+  Next next_a = {seg0, first - seg0 * per}, next_b = next_a;
+  auto step = [&](Next& n) __attribute__((always_inline)) {
+    if (++n.k == per) {
+      n.k = 0;
+      ++n.seg;
     }
-    if (PAIR == kPairSum && next_seg >= kTerms) {
-      a_at += a_second * 2;
-      second = true;
-    }
+  };
+  auto term_of = [&](const Next& n) __attribute__((always_inline)) {
+    return PAIR == kPairSum && n.seg >= kTerms ? n.seg - kTerms : n.seg;
+  };
+  auto from_a = [&](int s) __attribute__((always_inline)) {
+    int64_t at = next_a.k * a_step;
+    if constexpr (SIX) at += (kSixA >> (2 * term_of(next_a)) & 3) * p.a_planes.plane * 2;
+    if (PAIR == kPairSum && next_a.seg >= kTerms) at += a_second * 2;
     From f;
-    f.a = uniform(a0 + a_at);
-    f.b0 = uniform(static_cast<const unsigned char*>(second ? b_other : b_first) + b_at);
-    f.b1 = kTwo ? uniform(static_cast<const unsigned char*>(b_other) + b_at) : nullptr;
-    f.to = __builtin_amdgcn_readfirstlane(lds_at + (s % S) * C::kStageBytes);
-    f.k_left = static_cast<int>(p.K) - next_k * C::BK;
-    if (++next_k == per) {
-      next_k = 0;
-      ++next_seg;
-    }
+    f.p0 = uniform(a0 + at);
+    f.p1 = nullptr;
+    f.to = __builtin_amdgcn_readfirstlane(lds_at + (s % C::kAStages) * C::kABytes);
+    f.k_left = static_cast<int>(p.K) - next_a.k * C::BK;
+    step(next_a);
     return f;
   };
-  // Copy j (of kPerStage) of a wavefront; TAIL: the operands end in the stage.
-  auto issue = [&](const From& f, auto copy_j, auto tail) __attribute__((always_inline)) {
-    constexpr int j = decltype(copy_j)::value;
-    auto copy = [&](const unsigned char* base, uint32_t offset, uint32_t to, int piece_k)
-        __attribute__((always_inline)) {
-      if constexpr (!decltype(tail)::value) {
-        dma16_base(base, offset, to);
-      } else {
-        const unsigned char* at = piece_k < f.k_left ? base + offset : kZeros;
-        dma16_asm(at, reinterpret_cast<unsigned char*>(static_cast<uintptr_t>(to)));
-      }
-    };
-    if constexpr (j < C::kALoads) {
-      const int q = wave * C::kALoads + j;
-      copy(f.a, a_off[j], f.to + q * 1024, typename P::PA(q, lane).k);
+  auto from_b = [&](int s) __attribute__((always_inline)) {
+    int64_t at_b = b0 + next_b.k * b_step;
+    if constexpr (SIX) at_b += (kSixB >> (2 * term_of(next_b)) & 3) * p.b_planes[0].plane * 2;
+    const bool second = PAIR == kPairSum ? next_b.seg >= kTerms : PAIR == kPairTwo && at.which != 0;
+    From f;
+    f.p0 = uniform(static_cast<const unsigned char*>(second ? b_other : b_first) + at_b);
+    f.p1 = kTwo ? uniform(static_cast<const unsigned char*>(b_other) + at_b) : nullptr;
+    f.to = __builtin_amdgcn_readfirstlane(lds_at + C::kAStages * C::kABytes +
+                                          (s % C::kBStages) * C::kBBytes);
+    f.k_left = static_cast<int>(p.K) - next_b.k * C::BK;
+    step(next_b);
+    return f;
+  };
+  // Copy j of a wavefront; TAIL: the operand may end in the stage.
+  auto copy = [&](const From& f, const unsigned char* base, uint32_t offset, uint32_t to, int piece_k,
+                  auto tail) __attribute__((always_inline)) {
+    if constexpr (!decltype(tail)::value) {
+      dma16_base(base, offset, to);
     } else {
-      const int q = wave * C::kBLoads + j - C::kALoads;
-      copy(kTwo && q >= P::kBPieces ? f.b1 : f.b0, b_off[j - C::kALoads],
-           f.to + P::SA::kBytes + q * 1024, typename P::PB(q % P::kBPieces, lane).k);
+      const unsigned char* at = piece_k < f.k_left ? base + offset : kZeros;
+      dma16_asm(at, reinterpret_cast<unsigned char*>(static_cast<uintptr_t>(to)));
     }
   };
-  auto issue_all = [&](int s) __attribute__((always_inline)) {
-    const From f = from(s);
-    if (f.k_left >= C::BK)
-      each<kPerStage>([&](auto j) __attribute__((always_inline)) { issue(f, j, std::false_type()); });
-    else
-      each<kPerStage>([&](auto j) __attribute__((always_inline)) { issue(f, j, std::true_type()); });
+  auto copy_a = [&](const From& f, auto j, auto tail) __attribute__((always_inline)) {
+    const int q = wave * kACopies + j;
+    copy(f, f.p0, a_off[j], f.to + q * 1024, typename P::PA(q, lane).k, tail);
+  };
+  auto copy_b = [&](const From& f, auto j, auto tail) __attribute__((always_inline)) {
+    const int q = wave * kBCopies + j;
+    copy(f, kTwo && q >= P::kBPieces ? f.p1 : f.p0, b_off[j], f.to + q * 1024,
+         typename P::PB(q % P::kBPieces, lane).k, tail);
+  };
+  auto fill_a = [&](int s) __attribute__((always_inline)) {
+    if (s >= nk) return;
+    const From f = from_a(s);
+    each<kACopies>([&](auto j) __attribute__((always_inline)) { copy_a(f, j, std::true_type()); });
+  };
+  auto fill_b = [&](int s) __attribute__((always_inline)) {
+    if (s >= nk) return;
+    const From f = from_b(s);
+    each<kBCopies>([&](auto j) __attribute__((always_inline)) { copy_b(f, j, std::true_type()); });
   };
   // Fragment n (of kFrags) of step kk of stage s, in the order of their first use.
   constexpr int kFrags = C::kTm + C::kTn;
   auto read = [&](Frags<C>& f, int s, int kk, auto frag_n) __attribute__((always_inline)) {
     constexpr int n = decltype(frag_n)::value;
-    const unsigned char* As = lds + (s % S) * C::kStageBytes;
-    const unsigned char* Bs = As + P::SA::kBytes;
+    const unsigned char* As = lds + (s % C::kAStages) * C::kABytes;
+    const unsigned char* Bs = lds + C::kAStages * C::kABytes + (s % C::kBStages) * C::kBBytes;
     if constexpr (n < C::kTn) {
       f.b[n] = frag_bf16<typename P::SB, P::kB>(
           Bs + (kTwo ? n / (C::kTn / 2) * P::SB::kBytes : 0),
@@ -254,61 +266,111 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
   constexpr int kMma = C::kTm * C::kTn;
   // (reads at the front: the last are back when a barrier follows)
   constexpr int kReadMma = kFrags < kMma ? kFrags : kMma;
-  enum { kNoCopies, kWholeCopies, kAnyCopies };  // any: a stage with a tail, or none
+  // Copies come in rounds: round s fills B of stage s + kBStages, then A of
+  // stage s + kAStages, from the last phase of stage s to the third of the
+  // next, evenly: the address unit has 27 cycles of work for each of the 64
+  // copies that a compute unit makes in a stage of 2048 cycles.
+  enum { kNoCopies, kWholeCopies, kAnyCopies };  // any: stages with a tail, or none
   using None = std::integral_constant<int, kNoCopies>;
   using Whole = std::integral_constant<int, kWholeCopies>;
   using Any = std::integral_constant<int, kAnyCopies>;
-  auto phase = [&](const Frags<C>& f, Frags<C>& next, int rs, int rkk, int cs, auto copies)
+  constexpr int kCopies = kACopies + kBCopies;
+  From fa, fb;
+  bool has_a = false, has_b = false;
+  auto start_round = [&](int s, auto copies) __attribute__((always_inline)) {
+    if constexpr (decltype(copies)::value == kWholeCopies) {
+      fb = from_b(s + C::kBStages);
+      fa = from_a(s + C::kAStages);
+    } else {
+      has_b = s + C::kBStages < nk;
+      has_a = s + C::kAStages < nk;
+      if (has_b) fb = from_b(s + C::kBStages);
+      if (has_a) fa = from_a(s + C::kAStages);
+    }
+  };
+  // part: 0 to 3, the phase of the round.
+  auto phase = [&](const Frags<C>& f, Frags<C>& next, int rs, int rkk, auto part, auto copies)
       __attribute__((always_inline)) {
-    constexpr int kCopies = decltype(copies)::value;
-    From stage;
-    if constexpr (kCopies == kWholeCopies) stage = from(cs);
-    if constexpr (kCopies == kAnyCopies)
-      if (cs < nk) stage = from(cs);
+    constexpr int kHow = decltype(copies)::value;
     each<kMma>([&](auto m) __attribute__((always_inline)) {
       constexpr int i = m / C::kTn, j = m % C::kTn;
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
       each<kFrags>([&](auto n) __attribute__((always_inline)) {
         if constexpr (n * kReadMma / kFrags == m) read(next, rs, rkk, n);
       });
-      each<kPerStage>([&](auto c) __attribute__((always_inline)) {
-        if constexpr (kCopies == kWholeCopies && c * kMma / kPerStage == m)
-          issue(stage, c, std::false_type());
-        if constexpr (kCopies == kAnyCopies && c * kMma / kPerStage == m)
-          if (cs < nk) issue(stage, c, std::true_type());
+      each<kCopies>([&](auto c) __attribute__((always_inline)) {
+        constexpr int kSlot = c * (4 * kMma - kMma / 2) / kCopies;
+        if constexpr (kHow != kNoCopies && kSlot == decltype(part)::value * kMma + m) {
+          using Tail = std::integral_constant<bool, kHow == kAnyCopies>;
+          if constexpr (c < kBCopies) {
+            if (kHow == kWholeCopies || has_b) copy_b(fb, c, Tail());
+          } else {
+            if (kHow == kWholeCopies || has_a)
+              copy_a(fa, std::integral_constant<int, c - kBCopies>(), Tail());
+          }
+        }
       });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
+  using Part0 = std::integral_constant<int, 0>;
+  using Part1 = std::integral_constant<int, 1>;
+  using Part2 = std::integral_constant<int, 2>;
+  using Part3 = std::integral_constant<int, 3>;
   auto read_all = [&](Frags<C>& f, int s, int kk) __attribute__((always_inline)) {
     each<kFrags>([&](auto n) __attribute__((always_inline)) { read(f, s, kk, n); });
   };
-  auto body = [&](int s, auto copies) __attribute__((always_inline)) {
-    phase(f0, f1, s, 1, 0, None());
-    phase(f1, f0, s, 2, 0, None());
-    phase(f0, f1, s, 3, 0, None());
-    if (s + 1 < nk) {
-      // f1 is read, and at most stages s + 2 .. s + S - 1 are still in flight.
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
-      wait_stages<kPerStage, S - 2>(nk - 2 - s);
-      stage_barrier();
-    }
-    phase(f1, f0, s + 1, 0, s + S, copies);
+  // Before the last phase of stage s: its last fragments are in registers, and
+  // stage s + 1 is there.  Behind its B are A's copies of the same round and
+  // the rounds after it, up to s - 1.
+  auto meet = [&](int s) __attribute__((always_inline)) {
+    if (s + 1 >= nk) return;
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
+    if (s - 1 + C::kAStages < nk)
+      wait_vmcnt<(C::kBStages - 2) * kCopies + kACopies>();
+    else
+      wait_vmcnt<0>();
+    stage_barrier();
   };
+  // The last phase of stage s - 1 and the first three of stage s.
+  auto body = [&](int s, auto copies) __attribute__((always_inline)) {
+    start_round(s - 1, copies);
+    phase(f1, f0, s, 0, Part0(), copies);
+    phase(f0, f1, s, 1, Part1(), copies);
+    phase(f1, f0, s, 2, Part2(), copies);
+    phase(f0, f1, s, 3, Part3(), copies);
+    meet(s);
+  };
+  // The rounds before stage 0, without work.
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (s < nk) issue_all(s);
-  wait_stages<kPerStage, S - 1>(nk - 1);
+  for (int s = -C::kAStages; s < 0; ++s) {
+    if (s + C::kBStages >= 0) fill_b(s + C::kBStages);
+    fill_a(s + C::kAStages);
+  }
+  if (nk > C::kAStages)
+    wait_vmcnt<kCopies>();
+  else
+    wait_vmcnt<0>();
   stage_barrier();
-  read_all(f0, 0, 0);
-  // Runs of stages that fill whole ones, and single ones that fill a tail or nothing.
-  const bool tails = p.K % C::BK != 0;
-  for (int s = 0; s < nk;) {
-    int end = nk - S;
-    if (tails && s + (per - 1 - next_k) < end) end = s + (per - 1 - next_k);
-    for (; s < end; ++s) body(s, Whole());
-    body(s, Any());
-    ++s;
+  if (nk > 0) {
+    read_all(f0, 0, 0);
+    phase(f0, f1, 0, 1, Part1(), None());
+    phase(f1, f0, 0, 2, Part2(), None());
+    phase(f0, f1, 0, 3, Part3(), None());
+    meet(0);
+    // Runs of rounds that fill whole stages, and single ones that fill a tail or nothing.
+    const bool tails = p.K % C::BK != 0;
+    for (int s = 1; s < nk;) {
+      int end = nk - C::kAStages + 1;  // round s - 1 fills A of stage s - 1 + kAStages
+      if (tails) {
+        const int whole = per - 1 - (next_a.k > next_b.k ? next_a.k : next_b.k);
+        if (s + whole < end) end = s + whole;
+      }
+      for (; s < end; ++s) body(s, Whole());
+      if (s < nk) body(s, Any());
+      ++s;
+    }
+    mma_frags<C>(acc, f1);
   }
   __syncthreads();
   if constexpr (std::is_same<Epi, GatedEpilogue<uint16_t>>::value) {

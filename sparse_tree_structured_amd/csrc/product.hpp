@@ -25,9 +25,9 @@ Cut cut_product(const Product& p);
 Cut cut_whole(const Product& p);
 
 template <typename E> using TileAny = AnyCfg<E, 128, 256, 64, 64>;
-using TileBig = StepCfg<256, 256, 128, 64, 2>;
-using TileMid = StepCfg<128, 256, 64, 64, 3>;
-using TileSmall = StepCfg<128, 128, 64, 64, 2>;  // two workgroups a compute unit
+using TileBig = StepCfg<256, 256, 128, 64, 3>;
+using TileMid = StepCfg<128, 256, 64, 64, 4>;
+using TileSmall = StepCfg<128, 128, 64, 64, 3>;  // two workgroups a compute unit
 
 // The slices' sums through the epilogue (nothing where `bad` holds the call's number).
 template <class Epi>
