@@ -376,7 +376,8 @@ __global__ __launch_bounds__(C::kThreads) void product_direct_kernel(Product p, 
   if constexpr (std::is_same<Epi, GatedEpilogue<uint16_t>>::value) {
     gated_epilogue<C>(acc, lds, epi.e, m0, n0);
   } else if constexpr (std::is_same<Epi, LinearEpilogue<uint16_t, uint16_t>>::value) {
-    if (epi.e.save[0] || reinterpret_cast<uintptr_t>(epi.e.residual) % 16 != 0)
+    if (epi.e.save[0] ||
+        (epi.e.residual && (p.N % 8 != 0 || reinterpret_cast<uintptr_t>(epi.e.residual) % 16 != 0)))
       tile_epilogue<C>(acc, lds, epi, m0, p.M, n0, p.N, at.which);
     else
       linear_epilogue<C>(acc, lds, epi.e, m0, n0, at.which);

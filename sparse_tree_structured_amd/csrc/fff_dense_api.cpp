@@ -82,12 +82,17 @@ Product forward_product(const Shape& s, bool gated) {
   return p;
 }
 
-// da . W^T (gated: the two side by side in rows of 2N).
+// Rows of N as the workspace holds them: whole 16-byte pieces.
+int64_t da_ld(const Shape& s, bool gated) {
+  return gated || s.act != FFF_ACT_NONE ? fff::planes_ld(s.N) : s.N;
+}
+
+// da . W^T (gated: two, one matrix after the other).
 Product dx_product(const Shape& s, bool gated) {
   Product p = base(s, fff::kProductNT, gated ? fff::kPairSum : fff::kSingle);
   p.out_bf16 = p.bf16;
-  p.lda = gated ? 2 * int64_t(s.N) : s.N;
-  p.a_second = s.N;
+  p.lda = da_ld(s, gated);
+  p.a_second = s.T * p.lda;
   p.ldb = s.N;
   p.M = s.T;
   p.N = s.K;
@@ -101,8 +106,8 @@ Product dx_product(const Shape& s, bool gated) {
 Product dw_product(const Shape& s, bool gated) {
   Product p = base(s, fff::kProductTN, gated ? fff::kPairTwo : fff::kSingle);
   p.out_bf16 = s.grad_dtype == FFF_DTYPE_BF16;
-  p.lda = s.K;
-  p.ldb = gated ? 2 * int64_t(s.N) : s.N;
+  p.lda = s.x_dtype == FFF_DTYPE_E4M3 ? fff::planes_ld(s.K) : s.K;
+  p.ldb = da_ld(s, gated);
   p.M = s.K;
   p.N = s.N;
   p.K = s.T;
@@ -140,8 +145,9 @@ Layout backward_layout(const Shape& s, bool gated) {
     return here;
   };
   const size_t rows = static_cast<size_t>(s.T);
-  l.da = take(gated ? rows * s.N * 2 * e : s.act != FFF_ACT_NONE ? rows * s.N * e : 0);
-  l.x = take(s.x_dtype == FFF_DTYPE_E4M3 ? rows * s.K * e : 0);
+  const size_t row = size_t(da_ld(s, gated)) * e;
+  l.da = take(gated ? 2 * rows * row : s.act != FFF_ACT_NONE ? rows * row : 0);
+  l.x = take(s.x_dtype == FFF_DTYPE_E4M3 ? rows * fff::planes_ld(s.K) * e : 0);
   l.strips = take(gated ? 0 : fff::act_backward_partials(s.T, s.N, s.dtype == FFF_DTYPE_BF16) * 4);
   // (the word of values that are not finite, then the planes)
   l.planes = take(split_da(s, gated) ? 256 + (gated ? 2 : 1) * fff::planes_bytes(s.T, s.N) : 0);
@@ -220,14 +226,14 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
     px.bad = pw.bad = {reinterpret_cast<unsigned long long*>(ws + l.planes), fff::call_number()};
     give_planes(s, gated, ws + l.planes + 256, px, pw);
     if (!own_da) {
-      e = fff::launch_split(b.dy, s.T, s.N, px.a_planes, px.bad, stream);
+      e = fff::launch_split(b.dy, s.T, s.N, s.N, px.a_planes, px.bad, stream);
       if (e != hipSuccess) return FFF_ERROR_HIP;
     }
   }
   const bool restored = b.dW[0] && s.x_dtype == FFF_DTYPE_E4M3 && s.T > 0;
   if ((own_da && products && s.T > 0) || (b.h && s.T > 0) || b.dbias || restored) {
     fff::ActBackward a = {};
-    if (restored) a.x = {s.T, s.K, s.x_group, b.x, b.x_scale, ws + l.x};
+    if (restored) a.x = {s.T, s.K, s.x_group, b.x, b.x_scale, ws + l.x, fff::planes_ld(s.K)};
     a.T = s.T;
     a.N = s.N;
     a.bf16 = s.dtype == FFF_DTYPE_BF16;
@@ -241,6 +247,7 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
       }
       a.group = s.save_group ? s.save_group : s.N;
       a.da = products ? ws + l.da : nullptr;
+      a.da_ld = da_ld(s, gated);
       if (split) {
         a.da_planes[0] = pw.b_planes[0];
         a.da_planes[1] = pw.b_planes[1];
@@ -253,7 +260,7 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
     e = fff::launch_act_backward(a, stream);
     if (e != hipSuccess) return FFF_ERROR_HIP;
   }
-  const size_t half = size_t(s.N) * type_size(s.dtype);
+  const size_t second = size_t(s.T) * da_ld(s, gated) * type_size(s.dtype);
   if (b.dx && s.T > 0) {
     px.a = da;
     px.b[0] = b.W[0];
@@ -265,7 +272,7 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
   if (b.dW[0]) {
     pw.a = restored ? ws + l.x : b.x;
     pw.b[0] = da;
-    pw.b[1] = static_cast<const unsigned char*>(da) + half;
+    if (gated) pw.b[1] = static_cast<const unsigned char*>(da) + second;
     pw.e.out[0] = b.dW[0];
     pw.e.out[1] = b.dW[1];
     e = fff::launch_product(pw, ws + l.products, stream);

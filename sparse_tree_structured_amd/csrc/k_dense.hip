@@ -45,7 +45,8 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(const float* partial, i
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Whether the rows of both operands are whole 16-byte pieces.
+// Whether the rows of both operands are whole 16-byte pieces (K too: a longer
+// row's rest is zeros in the workspace's da only, which cut_product is told).
 bool direct_sizes(const Product& p) {
   if (p.lda % 8 != 0 || p.ldb % 8 != 0 || p.a_second % 8 != 0) return false;
   return p.kind == kProductTN || p.K % 8 == 0;
@@ -94,7 +95,7 @@ Cut cut_with(const Product& p, const TileSize& t, double& us) {
   return c;
 }
 
-Cut cut_direct(const Product& p) {
+Cut cut_direct(const Product& p, double* us_of = nullptr) {
   static const TileSize kTiles[] = {{kTileBig, 256, 256, 64, 4.9e12},
                                     {kTileMid, 128, 256, 64, 3.6e12},
                                     {kTileSmall, 128, 128, 64, 3.2e12}};
@@ -106,18 +107,19 @@ Cut cut_direct(const Product& p) {
     const Cut c = cut_with(p, t, us);
     if (t.tile == kTileBig || us < least) best = c, least = us;
   }
+  if (us_of) *us_of = least;
   return best;
 }
 
-Cut cut_any(const Product& p) {
-  double us;
-  return cut_with(p, {kTileAny, 128, 256, p.bf16 ? 32 : 16, p.bf16 ? 3e12 : 0.4e12}, us);
+Cut cut_any(const Product& p, double* us_of = nullptr) {
+  double own, &us = us_of ? *us_of : own;
+  return cut_with(p, {kTileAny, 128, 256, p.bf16 ? 32 : 16, p.bf16 ? 1.4e12 : 0.4e12}, us);
 }
 
 // Splits of x [rows, cols] float32 into planes: a lane has eight columns, the
 // row's padding among them.
-__global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t rows, int64_t cols, Planes out,
-                                                    NotFinite bad) {
+__global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t rows, int64_t cols, int64_t ld,
+                                                    Planes out, NotFinite bad) {
   const int64_t pieces = out.ld / 8;
   bool odd = false;
   for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < rows * pieces;
@@ -128,13 +130,49 @@ __global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t rows
     for (int h = 0; h < 8; h += 4) {
       const int64_t left = cols - col - h;
       Pack<float, 4> q;
-      q.load(x + row * cols + col + h, left < 4 ? static_cast<int>(left) : 4);
+      q.load(x + row * ld + col + h, left < 4 ? static_cast<int>(left) : 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[h + i] = q.get(i);
     }
     odd |= store_planes<8>(v, static_cast<uint16_t*>(out.at) + row * out.ld + col, out.plane, 8);
   }
   if (odd) *bad.word = bad.call;
+}
+
+// Copies x [rows, cols] bf16 to rows of `to_ld`, zeros behind the columns.
+__global__ __launch_bounds__(256) void pad_kernel(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
+                                                  uint16_t* to, int64_t to_ld) {
+  const int64_t pieces = to_ld / 8;
+  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < rows * pieces;
+       u += int64_t(gridDim.x) * 256) {
+    const int64_t row = u / pieces, col = u % pieces * 8;
+    const int64_t left = cols - col;
+    Pack<uint16_t, 8> q;
+    q.load(x + row * ld + col, left < 8 ? static_cast<int>(left) : 8);
+    q.store(to + row * to_ld + col, 8);
+  }
+}
+
+hipError_t launch_pad(const void* x, int64_t rows, int64_t cols, int64_t ld, void* to, int64_t to_ld,
+                      hipStream_t st) {
+  const int64_t blocks = ceil_div(rows * (to_ld / 8), 256);
+  pad_kernel<<<dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st>>>(
+      static_cast<const uint16_t*>(x), rows, cols, ld, static_cast<uint16_t*>(to), to_ld);
+  return hipGetLastError();
+}
+
+// Which operands of a bf16 product do not have rows of whole pieces.
+struct Padding {
+  bool a, b;
+};
+Padding padding_of(const Product& p) {
+  return {p.lda % 8 != 0, p.ldb % 8 != 0};
+}
+
+// Whether the operands but those that are copied are aligned.
+bool operands_aligned(const Product& p, const Padding& copied) {
+  if (!copied.a && !aligned16(p.a)) return false;
+  return copied.b || (aligned16(p.b[0]) && (p.pair == kSingle || aligned16(p.b[1])));
 }
 
 size_t cut_bytes(const Product& p, const Cut& c) {
@@ -184,18 +222,17 @@ bool split_wanted(const Product& p) {
   return flops / 90e6 > 6 * flops / 900e6 + 10 * elements / 4e6 + 25.0;
 }
 
-hipError_t launch_split(const void* x, int64_t rows, int64_t cols, const Planes& out,
+hipError_t launch_split(const void* x, int64_t rows, int64_t cols, int64_t ld, const Planes& out,
                         const NotFinite& bad, hipStream_t st) {
   const int64_t blocks = ceil_div(rows * (out.ld / 8), 256);
   split_kernel<<<dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st>>>(
-      static_cast<const float*>(x), rows, cols, out, bad);
+      static_cast<const float*>(x), rows, cols, ld, out, bad);
   return hipGetLastError();
 }
 
 Cut cut_product(const Product& p) {
   if (!p.bf16) return p.bad.word ? cut_direct(p) : cut_any(p);
-  const bool direct = direct_sizes(p) && aligned16(p.a) && aligned16(p.b[0]) && aligned16(p.b[1]);
-  return direct ? cut_direct(p) : cut_any(p);
+  return p.padded || (direct_sizes(p) && operands_aligned(p, {})) ? cut_direct(p) : cut_any(p);
 }
 
 bool product_fits(const Product& p) {
@@ -242,19 +279,57 @@ PlanesAt planes_at(const Product& p) {
   return l;
 }
 
-hipError_t split_operand(const void* x, int64_t rows, int64_t cols, unsigned char* to, Planes& out,
-                         const NotFinite& bad, hipStream_t st) {
+hipError_t split_operand(const void* x, int64_t rows, int64_t cols, int64_t ld, unsigned char* to,
+                         Planes& out, const NotFinite& bad, hipStream_t st) {
   out = {to, planes_ld(cols), rows * planes_ld(cols)};
-  return launch_split(x, rows, cols, out, bad, st);
+  return launch_split(x, rows, cols, ld, out, bad, st);
 }
+
+// Whether copies with padded rows, for the tiles straight into LDS, are worth
+// their time: 1514 x 3869 x 2 x 1885 takes 90 us instead of 234.
+bool padding_wanted(const Product& p) {
+  if (!p.bf16) return false;
+  const Padding pad = padding_of(p);
+  if (!pad.a && !pad.b) return false;
+  int64_t rows, cols;
+  double us = 0, direct = 0, any = 0;
+  a_sizes(p, rows, cols);
+  if (pad.a) us += 4.0 + 4.0 * rows * cols / 4e6;
+  b_sizes(p, rows, cols);
+  if (pad.b) us += (p.pair == kSingle ? 1 : 2) * (4.0 + 4.0 * rows * cols / 4e6);
+  cut_direct(p, &direct);
+  cut_any(p, &any);
+  return us + direct < any;
+}
+
+PlanesAt padded_at(const Product& p) {
+  PlanesAt l = {};
+  const Padding pad = padding_of(p);
+  int64_t rows, cols;
+  l.bytes = padded(cut_bytes(p, cut_direct(p)));
+  a_sizes(p, rows, cols);
+  if (pad.a) {
+    l.a = l.bytes;
+    l.bytes += padded(size_t(rows) * planes_ld(cols) * 2);
+  }
+  b_sizes(p, rows, cols);
+  for (int i = 0; pad.b && i < (p.pair == kSingle ? 1 : 2); ++i) {
+    l.b[i] = l.bytes;
+    l.bytes += padded(size_t(rows) * planes_ld(cols) * 2);
+  }
+  return l;
+}
+
 
 }  // namespace
 
 // For pointers of any alignment.
 size_t product_workspace(const Product& p) {
   size_t most = cut_bytes(p, cut_any(p));
-  const size_t direct = p.bf16 ? (direct_sizes(p) ? cut_bytes(p, cut_direct(p)) : 0)
-                               : (split_wanted(p) ? planes_at(p).bytes : 0);
+  const size_t direct = !p.bf16           ? (split_wanted(p) ? planes_at(p).bytes : 0)
+                        : direct_sizes(p)   ? cut_bytes(p, cut_direct(p))
+                        : padding_wanted(p) ? padded_at(p).bytes
+                                            : 0;
   const size_t small = small_product(p) ? small_workspace(p) : 0;
   if (direct > most) most = direct;
   return small > most ? small : most;
@@ -268,6 +343,27 @@ hipError_t launch_product(const Product& product, void* workspace, hipStream_t s
     p.bad = {};
     return launch_small(p, workspace, st);
   }
+  const Padding pad = padding_of(p);
+  if (padding_wanted(p) && operands_aligned(p, pad)) {
+    unsigned char* const ws = static_cast<unsigned char*>(workspace);
+    const PlanesAt l = padded_at(p);
+    int64_t rows, cols;
+    hipError_t e = hipSuccess;
+    a_sizes(p, rows, cols);
+    if (pad.a) {
+      e = launch_pad(p.a, rows, cols, p.lda, ws + l.a, planes_ld(cols), st);
+      p.a = ws + l.a;
+      p.lda = planes_ld(cols);
+    }
+    b_sizes(p, rows, cols);
+    for (int i = 0; pad.b && i < (p.pair == kSingle ? 1 : 2) && e == hipSuccess; ++i) {
+      e = launch_pad(p.b[i], rows, cols, p.ldb, ws + l.b[i], planes_ld(cols), st);
+      p.b[i] = ws + l.b[i];
+    }
+    if (pad.b) p.ldb = planes_ld(cols);
+    p.padded = true;
+    if (e != hipSuccess) return e;
+  }
   if (!split_wanted(p)) {
     p.bad = {};
   } else {
@@ -279,12 +375,12 @@ hipError_t launch_product(const Product& product, void* workspace, hipStream_t s
       p.bad = {reinterpret_cast<unsigned long long*>(ws + l.word), call_number()};
     if (!p.a_planes.at) {
       a_sizes(p, rows, cols);
-      e = split_operand(p.a, rows, cols, ws + l.a, p.a_planes, p.bad, st);
+      e = split_operand(p.a, rows, cols, p.lda, ws + l.a, p.a_planes, p.bad, st);
     }
     b_sizes(p, rows, cols);
     for (int i = 0; i < (p.pair == kSingle ? 1 : 2); ++i)
       if (e == hipSuccess && !p.b_planes[i].at)
-        e = split_operand(p.b[i], rows, cols, ws + l.b[i], p.b_planes[i], p.bad, st);
+        e = split_operand(p.b[i], rows, cols, p.ldb, ws + l.b[i], p.b_planes[i], p.bad, st);
     if (e != hipSuccess) return e;
   }
   if (p.kind == kProductNN) return run_nn(p, workspace, st);

@@ -60,7 +60,7 @@ __device__ __forceinline__ void restore_rows(const Restore& r, int64_t block, in
     q.template load<false>(r.codes, r.scale, r.group ? r.group : r.d, t, col, r.d, n);
     float v[V];
     q.get(v, true);
-    if (n > 0) packed<E, V>(v).store(static_cast<E*>(r.x) + t * r.d + col, n);
+    if (n > 0) packed<E, V>(v).store(static_cast<E*>(r.x) + t * r.ld + col, n);
   }
 }
 
@@ -107,6 +107,16 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
   bool odd = false;
   // (with planes a row's padding is zeros in them)
   const int n_plane = a.da_planes[0].at ? there(a.da_planes[0].ld - col, V) : 0;
+  const int n_da = there(a.da_ld - col, V);
+  auto store_da = [&](int which, float (&v)[V], size_t row) {
+    if (!a.da || n_da <= 0) return;
+    if (n < V) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = i < n ? v[i] : 0.0f;
+    }
+    packed<E, V>(v).store(
+        static_cast<E*>(a.da) + (which * static_cast<size_t>(a.T) + row) * a.da_ld + col, n_da);
+  };
   auto planes = [&](int which, const float (&v)[V], size_t row) {
     if constexpr (sizeof(E) == 4)
       if (n_plane > 0)
@@ -137,14 +147,10 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
         }
         planes(0, da, row);
         planes(1, du, row);
-        if (n > 0) {
-          if (a.da) {
-            E* out = static_cast<E*>(a.da) + row * (2 * size_t(a.N)) + col;
-            packed<E, V>(da).store(out, n);
-            packed<E, V>(du).store(out + a.N, n);
-          }
-          if (a.h) packed<E, V>(h).template store<true>(static_cast<E*>(a.h) + row * a.N + col, n);
-        }
+        store_da(0, da, row);
+        store_da(1, du, row);
+        if (a.h && n > 0)
+          packed<E, V>(h).template store<true>(static_cast<E*>(a.h) + row * a.N + col, n);
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -157,7 +163,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int co
           total[i] += da[i];
         }
         planes(0, da, row);
-        if (a.da && n > 0) packed<E, V>(da).store(static_cast<E*>(a.da) + row * a.N + col, n);
+        store_da(0, da, row);
       }
     }
   }
@@ -312,7 +318,7 @@ hipError_t launch_checkpoint_save(int64_t T, int d, bool bf16, int group, const 
 
 hipError_t launch_checkpoint_load(int64_t T, int d, bool bf16, int group, const void* codes,
                                   const float* scale, void* x, hipStream_t st) {
-  const Restore r = {T, d, group, codes, scale, x};
+  const Restore r = {T, d, group, codes, scale, x, d};
   const int grid = restore_grid(r, bf16);
   if (bf16)
     checkpoint_load_kernel<uint16_t><<<grid, 256, 0, st>>>(r);

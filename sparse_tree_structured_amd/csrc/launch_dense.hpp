@@ -78,12 +78,13 @@ struct Product {
   Planes a_planes, b_planes[2];
   int64_t a_planes_second;
   NotFinite bad;
+  bool padded;  // bf16: the rows have zeros up to whole 16-byte pieces
 };
 
 // Whether a float32 product is worth its operands' split into planes.
 bool split_wanted(const Product& p);
-// x [rows, cols] float32 into planes.
-hipError_t launch_split(const void* x, int64_t rows, int64_t cols, const Planes& out,
+// x, rows of ld floats, cols of them there, into planes.
+hipError_t launch_split(const void* x, int64_t rows, int64_t cols, int64_t ld, const Planes& out,
                         const NotFinite& bad, hipStream_t st);
 
 // Whether its tiles fit one launch.
@@ -98,7 +99,8 @@ struct Restore {
   int d, group;
   const void* codes;
   const float* scale;
-  void* x;  // null: none
+  void* x;     // null: none
+  int64_t ld;  // elements from a row of x to the next
 };
 
 // Elementwise part of the backward passes, column sums, and the x they need,
@@ -113,7 +115,9 @@ struct ActBackward {
   const void* save[2];    // pre-activation (gated: gate, up), or null where act is none
   const float* scale[2];  // of 8-bit saves, or null
   int group;
-  void* da;               // [T,N], gated [T,2N] (gate's gradient, then up's); or null
+  void* da;               // [T] rows of da_ld elements, zeros behind the N; gated: the gate's,
+                          // then up's; or null
+  int64_t da_ld;
   void* h;                // gated: act(gate) * up [T,N], or null
   float* dbias;           // [N] sums over rows of da, or null
   float* partial;         // workspace of dbias
