@@ -56,6 +56,8 @@ struct TileSize {
   ProductTile tile;
   int m, n, bk;
   double rate;  // of its matrix-core work, FLOP/s of a compute unit
+  int together = 1;      // workgroups of a compute unit that hide each other's steps
+  double step_us = 0.25;  // the shortest time of a step
 };
 
 // The time of a product in one kind of tile and number of slices, in us: what
@@ -63,9 +65,10 @@ struct TileSize {
 // tiles, and for slices a second launch and the sums' way through memory.
 double time_of(const Product& p, const TileSize& t, int64_t tiles, int64_t total, int64_t slices) {
   const int64_t steps = ceil_div(total, slices);
-  const int64_t rounds = ceil_div(tiles * slices, 256);
-  const double step = 2.0 * t.m * t.n * t.bk / t.rate * 1e6;
-  double us = rounds * (steps * (step > 0.25 ? step : 0.25) + 4.0);
+  const int64_t each = ceil_div(tiles * slices, 256);  // of the busiest compute unit
+  const int64_t rounds = ceil_div(each, t.together);
+  const double busy = 2.0 * t.m * t.n * t.bk / t.rate * 1e6 * (each < t.together ? each : t.together);
+  double us = rounds * (steps * (busy > t.step_us ? busy : t.step_us) + 4.0);
   if (slices > 1) {
     const int products = p.pair == kPairColumns || p.pair == kPairTwo ? 2 : 1;
     us += 5.0 + 8.0 * slices * products * p.M * p.N / 4e6;
@@ -82,11 +85,11 @@ Cut cut_with(const Product& p, const TileSize& t, double& us) {
   int64_t tiles = c.tiles_m * c.tiles_n * (p.pair == kPairTwo ? 2 : 1);
   if (tiles < 1) tiles = 1;
   int64_t total = ceil_div(p.K, t.bk) * (p.pair == kPairSum ? 2 : 1);
-  if (!p.bf16 && t.tile != kTileAny) total *= 6;  // on planes
+  if (!p.bf16 && t.tile >= kTileBig) total *= 6;  // on planes
   int64_t slices = 1;
   us = time_of(p, t, tiles, total, 1);
   // Slices of at least four steps while tiles leave compute units idle.
-  for (int64_t s = 2; s * tiles <= 512 && s * 4 <= total; ++s) {
+  for (int64_t s = 2; s * tiles <= 512 * t.together && s * 4 <= total; ++s) {
     const double with = time_of(p, t, tiles, total, s);
     if (with < us) us = with, slices = s;
   }
@@ -113,7 +116,15 @@ Cut cut_direct(const Product& p, double* us_of = nullptr) {
 
 Cut cut_any(const Product& p, double* us_of = nullptr) {
   double own, &us = us_of ? *us_of : own;
-  return cut_with(p, {kTileAny, 128, 256, p.bf16 ? 32 : 16, p.bf16 ? 1.4e12 : 0.4e12}, us);
+  Cut c = cut_with(p, {kTileAny, 128, 256, p.bf16 ? 32 : 16, p.bf16 ? 1.4e12 : 0.45e12}, us);
+  // Float32 steps of the large tile take 2 us each: small products are spread
+  // further (512 x 512 x 2048 33 -> 16 us).
+  if (!p.bf16 && p.pair != kPairColumns) {
+    double small;
+    const Cut s = cut_with(p, {kTileAnySmall, 64, 128, 16, 0.5e12, 4, 0.95}, small);
+    if (small < us) c = s, us = small;
+  }
+  return c;
 }
 
 // Splits of x [rows, cols] float32 into planes: a lane has eight columns, the
@@ -205,9 +216,8 @@ FFF_SUM(LinearF32);
 
 Cut cut_whole(const Product& p) {
   Cut c = cut_any(p);
-  const int64_t total = ceil_div(p.K, p.bf16 ? 32 : 16) * (p.pair == kPairSum ? 2 : 1);
+  c.steps *= c.slices;
   c.slices = 1;
-  c.steps = static_cast<int>(total);
   return c;
 }
 
@@ -219,7 +229,7 @@ bool split_wanted(const Product& p) {
   const double pairs = p.pair == kSingle ? 1 : 2;
   const double flops = 2.0 * pairs * p.M * p.N * p.K;
   const double elements = double(p.M) * p.K * (p.pair == kPairSum ? 2 : 1) + pairs * p.K * p.N;
-  return flops / 90e6 > 6 * flops / 900e6 + 10 * elements / 4e6 + 25.0;
+  return flops / 90e6 > 6 * flops / 1100e6 + 10 * elements / 4e6 + 20.0;
 }
 
 hipError_t launch_split(const void* x, int64_t rows, int64_t cols, int64_t ld, const Planes& out,

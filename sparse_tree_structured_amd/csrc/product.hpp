@@ -10,9 +10,10 @@
 
 namespace fff {
 
-// Kernels: register staged (any sizes, types and alignment), or straight into
-// LDS with tiles of 256 x 256, 128 x 256 or 128 x 128.
-enum ProductTile { kTileAny, kTileBig, kTileMid, kTileSmall };
+// Kernels: register staged (any sizes, types and alignment) with tiles of 128 x
+// 256 or, float32, 64 x 128, or straight into LDS with tiles of 256 x 256, 128
+// x 256 or 128 x 128.
+enum ProductTile { kTileAny, kTileAnySmall, kTileBig, kTileMid, kTileSmall };
 
 struct Cut {
   ProductTile tile;
@@ -25,6 +26,7 @@ Cut cut_product(const Product& p);
 Cut cut_whole(const Product& p);
 
 template <typename E> using TileAny = AnyCfg<E, 128, 256, 64, 64>;
+using TileAnySmall = AnyCfg<float, 64, 128, 32, 64>;
 using TileBig = StepCfg<256, 256, 128, 64, 3>;
 using TileMid = StepCfg<128, 256, 64, 64, 4>;
 using TileSmall = StepCfg<128, 128, 64, 64, 3>;  // two workgroups a compute unit
@@ -65,15 +67,17 @@ hipError_t launch_direct(const Product& p, const Epi& epi, const Cut& c, hipStre
 
 template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
 hipError_t launch_cut(const Product& p, const Epi& epi, const Cut& c, hipStream_t st) {
-  if constexpr (sizeof(E) == 2) {
-    if (c.tile != kTileAny) return launch_direct<false, KIND, PAIR>(p, epi, c, st);
-  } else {
-    if (c.tile != kTileAny) return launch_direct<true, KIND, PAIR>(p, epi, c, st);
-  }
-  using C = TileAny<E>;
   constexpr bool kTwo = PAIR == kPairColumns;
-  return launch_tiles(product_any_kernel<E, KIND, PAIR, C, Epi>, AnyParts<E, KIND, kTwo, C>::kLds,
-                      C::kThreads, p, epi, c, st);
+  auto any = [&](auto cfg) {
+    using C = decltype(cfg);
+    return launch_tiles(product_any_kernel<E, KIND, PAIR, C, Epi>, AnyParts<E, KIND, kTwo, C>::kLds,
+                        C::kThreads, p, epi, c, st);
+  };
+  if (c.tile == kTileAny) return any(TileAny<E>());
+  if constexpr (sizeof(E) == 4 && !kTwo) {
+    if (c.tile == kTileAnySmall) return any(TileAnySmall());
+  }
+  return launch_direct<sizeof(E) == 4, KIND, PAIR>(p, epi, c, st);
 }
 
 template <typename E, ProductKind KIND, ProductPair PAIR, class Epi>
