@@ -11,6 +11,14 @@ float32 or 8 bits.
 
     python examples/train_block.py --steps 60 --bits 8
 
+With --layer gated the blocks have the dense layer in the FFF layer's place,
+
+    y = (silu(h . W_gate) * (h . W_up)) . W_down
+
+by gated and linear, and everything that its backward pass needs (h, and the
+sums of both projections) is kept in 8 bits; the product's own output is made
+again from them.
+
 The task is synthetic: targets are a fixed random function of the inputs.
 Prints the loss and the gradient's norm; returns them from train().
 """
@@ -30,12 +38,17 @@ BF16, F32 = torch.bfloat16, torch.float32
 class Model:
     """Parameters by name, with a float32 master and a gradient of each."""
 
-    def __init__(self, layers, d, P, D, h, device, gen):
+    def __init__(self, layers, d, P, D, h, device, gen, layer="fff"):
         N = 2 ** (D + 1) - 1
-        self.layers = layers
+        self.layers, self.kind = layers, layer
         init = {}
         for i in range(layers):
             init[f"{i}.gain"] = torch.ones(d)
+            if layer == "gated":  # P * h wide
+                for k in ("W_gate", "W_up"):
+                    init[f"{i}.{k}"] = torch.randn(d, P * h, generator=gen) / math.sqrt(d)
+                init[f"{i}.W_down"] = torch.randn(P * h, d, generator=gen) / math.sqrt(P * h)
+                continue
             init[f"{i}.W_node"] = torch.randn(P, N, d, generator=gen) / math.sqrt(d)
             init[f"{i}.b_node"] = 0.1 * torch.randn(P, N, generator=gen)
             init[f"{i}.V_node"] = torch.randn(P, N, h, generator=gen) / math.sqrt(h)
@@ -48,6 +61,9 @@ class Model:
     def layer(self, i):
         return [self.weight[f"{i}.{k}"] for k in ("W_node", "b_node", "V_node", "W_out")]
 
+    def dense(self, i):
+        return [self.weight[f"{i}.{k}"] for k in ("W_gate", "W_up", "W_down")]
+
     def forward(self, stream):
         """The output, and what the backward pass needs of each block."""
         saved, y = [], None
@@ -58,6 +74,12 @@ class Model:
             else:
                 n = fff.rms_norm(y, gain, residual=stream, want_rstd=True)
                 stream = n.residual_out
+            if i < self.layers and self.kind == "gated":
+                gate, up, down = self.dense(i)
+                g = fff.gated(n.y, gate, up, save="e4m3")
+                saved.append((stream, n.rstd, (fff.checkpoint(n.y), g.gate, g.up)))
+                y = fff.linear(g.h, down).y
+                continue
             saved.append((stream, n.rstd, n.y))
             if i == self.layers:
                 return n.y, saved
@@ -69,12 +91,26 @@ class Model:
         g = fff.rms_norm_backward(dout, stream, self.weight["gain"], rstd, dweight=self.grad["gain"])
         for i in reversed(range(self.layers)):
             stream, rstd, h = saved[i]
+            if self.kind == "gated":
+                dx = self.dense_backward(i, g.dx, *h)
+                g = fff.rms_norm_backward(dx, stream, self.weight[f"{i}.gain"], rstd, dresidual=g.dz,
+                                          dweight=self.grad[f"{i}.gain"])
+                continue
             out = {f"d{k}": self.grad[f"{i}.{k}"] for k in ("W_node", "b_node", "V_node", "W_out")}
             out["dx"] = torch.empty_like(h)
             fff.backward(h, *self.layer(i), g.dx, out=out)
             g = fff.rms_norm_backward(out["dx"], stream, self.weight[f"{i}.gain"], rstd,
                                       dresidual=g.dz, dweight=self.grad[f"{i}.gain"])
         return g.dz
+
+    def dense_backward(self, i, dy, h, gate, up):
+        """The dense layer's gradients from dy and what forward kept."""
+        w_gate, w_up, w_down = self.dense(i)
+        dprod = fff.linear_backward(dy, None, w_down, want_dW=False).dx
+        o = fff.gated_backward(dprod, h, w_gate, w_up, gate, up, want_h=True,
+                               dW_gate=self.grad[f"{i}.W_gate"], dW_up=self.grad[f"{i}.W_up"])
+        fff.linear_backward(dy, o.h, w_down, want_dx=False, dW=self.grad[f"{i}.W_down"])
+        return o.dx
 
     def optimiser(self, bits, weight_decay):
         """The optimiser's table (matrices decay, gains and biases do not)."""
@@ -88,10 +124,10 @@ class Model:
 
 
 def train(steps=60, layers=2, T=512, d=256, P=4, D=3, h=64, bits=8, lr=2e-3, seed=0, device="cuda:0",
-          log=None):
+          log=None, layer="fff"):
     """[(loss, gradient norm)] of every step."""
     gen = torch.Generator().manual_seed(seed)
-    model = Model(layers, d, P, D, h, device, gen)
+    model = Model(layers, d, P, D, h, device, gen, layer)
     stream = torch.randn(T, d, generator=gen).to(device)
     target = torch.tanh(stream @ (torch.randn(d, d, generator=gen) / math.sqrt(d)).to(device))
     table = model.optimiser(bits, weight_decay=0.01)
@@ -115,8 +151,9 @@ def main():
     ap.add_argument("--layers", type=int, default=2)
     ap.add_argument("--tokens", type=int, default=512)
     ap.add_argument("--bits", type=int, default=8, choices=[8, 32])
+    ap.add_argument("--layer", default="fff", choices=["fff", "gated"])
     a = ap.parse_args()
-    train(a.steps, a.layers, a.tokens, bits=a.bits, log=print)
+    train(a.steps, a.layers, a.tokens, bits=a.bits, log=print, layer=a.layer)
 
 
 if __name__ == "__main__":
