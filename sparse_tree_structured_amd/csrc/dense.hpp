@@ -44,16 +44,19 @@ __device__ __forceinline__ float activation(float a, int act) {
 // The activation and its derivative.
 __device__ __forceinline__ void activation_slope(float a, int act, float& value, float& slope) {
   switch (act) {
+    // (where q is 0 or 1 the second term is nothing, but its factors may be
+    // infinite: values beyond 1e19, infinities)
     case kActGelu: {
       const float q = logistic(kGelu2 * (a + kGelu3 * (a * a * a)));
       value = a * q;
-      slope = q + value * (1.0f - q) * (kGelu2 * (1.0f + 3.0f * kGelu3 * (a * a)));
+      const float more = value * (1.0f - q) * (kGelu2 * (1.0f + 3.0f * kGelu3 * (a * a)));
+      slope = q * (1.0f - q) == 0.0f ? q : q + more;
       break;
     }
     case kActSilu: {
       const float q = logistic(a);
       value = a * q;
-      slope = q + value * (1.0f - q);
+      slope = q * (1.0f - q) == 0.0f ? q : q + value * (1.0f - q);
       break;
     }
     case kActRelu:

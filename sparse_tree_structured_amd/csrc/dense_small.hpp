@@ -45,7 +45,9 @@ __device__ __forceinline__ bool finishes(const SmallArrival& a, int block, int s
                                          int lane) {
   unsigned long long* w = a.words + static_cast<size_t>(block) * (slices + 1);
   if (lane == 0) __hip_atomic_store(w + slice, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("" ::: "memory");
   wait_vmcnt<0>();  // it is in memory
+  asm volatile("" ::: "memory");
   unsigned long long there = a.call;
   if (lane < slices) there = __hip_atomic_load(w + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (__ballot(there != a.call) != 0) return false;
@@ -276,6 +278,7 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void product_small_kernel(Prod
   }
   if (slices == 1 || arrival.call == 0) return;
   // Every wavefront's sums are in memory before the workgroup arrives.
+  asm volatile("" ::: "memory");
   wait_vmcnt<0>();
   __syncthreads();
   if (wave == 0) {

@@ -484,3 +484,44 @@ def test_gradients_against_differences(act):
                          ("linear", 0, p.dx), ("linear", 1, p.dW), ("linear", 3, p.dbias)):
         want = differences(kind, k)
         assert float((got.to(F64) - want).norm() / want.norm()) < 1e-5, (kind, k)
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["gelu", "silu", "relu"])
+def test_slopes_of_large_values(act, ty):
+    """Far from zero an activation is the value itself or nothing, and its
+    slope 1 or 0, up to infinity."""
+    say("large values", act, ty)
+    at = torch.tensor([1e2, 1e10, 1e19, 1e20, 3e38, math.inf], device=DEV)
+    pre = torch.cat([at, -at]).to(TY[ty]).expand(5, 12).contiguous()
+    dy, W = torch.full((5, 12), 2.0, dtype=TY[ty], device=DEV), torch.eye(12, dtype=TY[ty], device=DEV)
+    da = fff.linear_backward(dy, None, W, act=act, pre=pre, want_dW=False).dx
+    assert bool((da[:, :6] == 2.0).all()) and bool((da[:, 6:] == 0.0).all())
+    one = torch.ones_like(pre)
+    g = fff.gated_backward(dy, None, W, W, pre[:, :5].repeat(1, 3)[:, :12].contiguous(), one, act=act, want_dW=False,
+                           want_h=True)
+    # (dx is not compared: dup = dh * 3e38 = 6e38 is beyond float32, and infinite beside weights of 0)
+    assert torch.equal(g.h[:, :5], pre[:, :5])
+    y = fff.linear(pre[:, :5].contiguous(), torch.eye(5, dtype=TY[ty], device=DEV), act=act).y
+    assert torch.equal(y, pre[:, :5])
+    y = fff.linear(-pre[:, :5].contiguous(), torch.eye(5, dtype=TY[ty], device=DEV), act=act).y
+    assert bool((y == 0).all())
+
+
+def test_two_calls_at_once_and_stale_workspaces():
+    """Few rows with K cut: calls on two streams at once, and on workspaces that
+    hold whatever another call left there, its own words among it."""
+    gen = seeded("at once")
+    T, K, N = 3, 4096, 512
+    say("two at once")
+    x, W, r = randn(gen, T, K, ty="bf16"), randn(gen, K, N, ty="bf16"), randn(gen, T, N, ty="bf16")
+    want = fff.linear(x, W, residual=r).y
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.full((8 << 20,), 255, dtype=torch.uint8, device=DEV) for _ in streams]
+    torch.cuda.synchronize()
+    outs = [r.clone() for _ in range(40)]
+    torch.cuda.synchronize()
+    for i, y in enumerate(outs):
+        fff.linear(x, W, residual=y, y=y, workspace=spaces[i % 2], stream=streams[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in outs)
