@@ -6,6 +6,12 @@
 // there into two LDS buffers.  bf16 uses v_mfma_f32_32x32x16_bf16 on the
 // layouts of mfma_tile.hpp; float32 v_mfma_f32_32x32x2_f32, whose products
 // and sums are those of 32-bit arithmetic.
+//
+// Float32 is bound by its matrix operations (a compute unit's 128 x 256 x 16
+// step takes 1.9 us at full rate): 16384 x 8192 x 2048 runs at 120 TFLOP/s.
+// bf16 steps of 32 take 1.2 us, most of it addresses and guards, 0.9 PFLOP/s at
+// best: bf16 comes here where rows are not aligned and copies are not worth
+// their time.  Two steps' loads in registers changed nothing.
 #pragma once
 
 #include "dense.hpp"

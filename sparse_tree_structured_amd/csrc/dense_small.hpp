@@ -13,6 +13,10 @@
 // a slice's sums go to the workspace past the caches of one XCD, and the
 // workgroup that finds all slices of its columns there adds them in their
 // order and writes the output: one launch, and the same result on every call.
+// Bound by HBM and, for the smallest, by launch and latency: one token through
+// a bf16 pair of 2048 x 8192 reads 67 MB in 14.7 us a call (4.6 TB/s; a large
+// copy moves 4.8), 64 tokens take 19.6 (x's rows come from L2 in every
+// workgroup); 1 x 8192 x 2048 takes 8.3 us on the GPU, 10.9 a call.
 // (Counting arrivals with compare and exchange took 20 us of 35 where 16
 // slices meet; a second launch takes 4 us of the host's time.)
 #pragma once
