@@ -622,8 +622,9 @@ typedef struct fff_dense_shape {
     int64_t T;           /* rows, 0 <= T < 2^31 */
     int32_t K, N;        /* inputs and outputs (of each of a gated pair), 1 up to
                             FFF_DENSE_MAX_WIDTH; every tensor below 2^40 elements.
-                            FFF_ERROR_NOT_SUPPORTED beyond either, or where an
-                            output has 2^22 tiles of 128 x 128 or more */
+                            FFF_ERROR_NOT_SUPPORTED beyond a width, and for outputs
+                            of more tiles than a launch has (2^21 of 128 x 128
+                            always fit) */
     int32_t dtype;       /* F32 or BF16: x, weights, bias, dy, dx, dh, h */
     int32_t out_dtype;   /* linear: of residual and y, `dtype` or F32; gated: `dtype`
                             (the backward passes ignore it) */

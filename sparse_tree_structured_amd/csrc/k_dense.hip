@@ -251,9 +251,12 @@ Cut cut_product(const Product& p) {
 }
 
 bool product_fits(const Product& p) {
-  const Cut c = cut_any(p);
   // (a launch has fewer than 2^32 threads)
-  return c.tiles_m * c.tiles_n * c.slices * 2 < (int64_t(1) << 22);
+  auto fits = [&](const Cut& c) {
+    const int64_t threads = c.tile == kTileAnySmall || c.tile == kTileSmall ? 256 : 512;
+    return c.tiles_m * c.tiles_n * c.slices * (p.pair == kPairTwo ? 2 : 1) * threads < (int64_t(1) << 32);
+  };
+  return fits(cut_any(p)) && fits(cut_direct(p));
 }
 
 namespace {
