@@ -1140,11 +1140,20 @@ def _act_code(act) -> int:
 
 def _matrix(t, what):
     """The shape of a contiguous matrix."""
-    if len(t.shape) != 2:
-        raise ValueError(f"{what} must have 2 dimensions, got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have 2 dimensions, got shape {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return t.shape
+    return shape
+
+
+def _columns(t, what):
+    """Columns of what _tensor then checks as a whole."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have 2 dimensions, got shape {tuple(shape)}")
+    return shape[1]
 
 
 def _scales(T, d, group):
@@ -1168,7 +1177,9 @@ def _workspace(rt, workspace, need, like, stream):
         return workspace, _tensor(workspace, (have,), rt.u8, like, "workspace"), have
     if not need:
         return None, 0, 0
-    workspace = _empty(rt, (need,), rt.u8, like.device, stream)
+    # (an int for the size: a tuple takes longer)
+    workspace = rt.empty(need, dtype=rt.u8, device=like.device) if stream is None else \
+        _empty(rt, (need,), rt.u8, like.device, stream)
     return workspace, workspace.data_ptr(), need
 
 
@@ -1176,21 +1187,20 @@ def _output(rt, t, shape, dtype, like, what, stream):
     """An output tensor, made where there is none, and its pointer."""
     if t is not None:
         return t, _tensor(t, shape, dtype, like, what)
-    t = _empty(rt, shape, dtype, like.device, stream)
+    t = rt.empty(shape, dtype=dtype, device=like.device) if stream is None else \
+        _empty(rt, shape, dtype, like.device, stream)
     return t, t.data_ptr()
 
 
 def _save_kind(rt, save, group, ty, code):
     """Dtype code and group of what is saved."""
-    if save not in (None, "same", "e4m3"):
+    if save not in ("same", "e4m3"):
         raise ValueError(f'save must be None, "same" or "e4m3", got {save!r}')
     return (DTYPE_E4M3, group) if save == "e4m3" else (code, 0)
 
 
 def _saved(rt, save, group, shape, ty, like, stream):
     """A tensor or Checkpoint for saved sums, and its pointers."""
-    if save is None:
-        return None, 0, 0
     t = _empty(rt, shape, rt.f8 if save == "e4m3" else ty, like.device, stream)
     if save == "same":
         return t, t.data_ptr(), 0
@@ -1210,7 +1220,7 @@ def linear(x, W, bias=None, *, residual=None, act: str = "none", out_dtype=None,
     dtype, "e4m3" in 8 bits with a scale per ``group`` = 32, 64 or 128 columns."""
     rt = _rt()
     T, K = _matrix(x, "x [T,K]")
-    K2, N = _matrix(W, "W [K,N]")
+    N = _columns(W, "W [K,N]")
     ty = x.dtype
     code = _code(rt, ty)
     pw = _tensor(W, (K, N), ty, x, "W [K,N]")
@@ -1218,12 +1228,12 @@ def linear(x, W, bias=None, *, residual=None, act: str = "none", out_dtype=None,
     if out_dtype is None:
         out_dtype = residual.dtype if residual is not None else y.dtype if y is not None else ty
     pr = _tensor(residual, (T, N), out_dtype, x, "residual") if residual is not None else 0
-    save_code, save_group = _save_kind(rt, save, group, ty, code)
+    save_code, save_group = _save_kind(rt, save, group, ty, code) if save is not None else (code, 0)
     sizes, need = _dense("fff_linear", T, K, N, code, _code(rt, out_dtype), _act_code(act),
                          save_code, save_group, code, 0, code)
     handle = _here(rt, x, stream)
     y, py = _output(rt, y, (T, N), out_dtype, x, "y", stream)
-    pre, pp, ps = _saved(rt, save, group, (T, N), ty, x, stream)
+    pre, pp, ps = _saved(rt, save, group, (T, N), ty, x, stream) if save is not None else (None, 0, 0)
     workspace, pws, have = _workspace(rt, workspace, need, x, stream)
     st = (_lib or load_library()).fff_linear(sizes, x.data_ptr(), pw, pb, pr, py, pp, ps, pws, have,
                                              handle)
@@ -1242,7 +1252,7 @@ def linear_backward(dy, x, W, *, act: str = "none", pre=None, want_dx: bool = Tr
     ``grad_dtype``; dbias is float32.  Outputs that are passed are filled."""
     rt = _rt()
     T, N = _matrix(dy, "dy [T,N]")
-    K, N2 = _matrix(W, "W [K,N]")
+    K, _ = _matrix(W, "W [K,N]")
     ty = dy.dtype
     code, act_code = _code(rt, ty), _act_code(act)
     pw = _tensor(W, (K, N), ty, dy, "W [K,N]")
@@ -1282,18 +1292,21 @@ def gated(x, W_gate, W_up, *, act: str = "silu", save: Optional[str] = None, gro
     linear's does."""
     rt = _rt()
     T, d = _matrix(x, "x [T,d]")
-    d2, F = _matrix(W_gate, "W_gate [d,F]")
+    F = _columns(W_gate, "W_gate [d,F]")
     ty = x.dtype
     code = _code(rt, ty)
     pg = _tensor(W_gate, (d, F), ty, x, "W_gate [d,F]")
     pu = _tensor(W_up, (d, F), ty, x, "W_up [d,F]")
-    save_code, save_group = _save_kind(rt, save, group, ty, code)
+    save_code, save_group = _save_kind(rt, save, group, ty, code) if save is not None else (code, 0)
     sizes, need = _dense("fff_gated", T, d, F, code, code, _act_code(act), save_code, save_group, code,
                          0, code)
     handle = _here(rt, x, stream)
     h, ph = _output(rt, h, (T, F), ty, x, "h", stream)
-    gate, p0, s0 = _saved(rt, save, group, (T, F), ty, x, stream)
-    up, p1, s1 = _saved(rt, save, group, (T, F), ty, x, stream)
+    gate = up = None
+    p0 = s0 = p1 = s1 = 0
+    if save is not None:
+        gate, p0, s0 = _saved(rt, save, group, (T, F), ty, x, stream)
+        up, p1, s1 = _saved(rt, save, group, (T, F), ty, x, stream)
     workspace, pws, have = _workspace(rt, workspace, need, x, stream)
     st = (_lib or load_library()).fff_gated(sizes, x.data_ptr(), pg, pu, ph, p0, s0, p1, s1, pws, have,
                                             handle)
@@ -1313,7 +1326,7 @@ def gated_backward(dh, x, W_gate, W_up, gate, up, *, act: str = "silu", want_dx:
     ``grad_dtype``.  Outputs that are passed are filled."""
     rt = _rt()
     T, F = _matrix(dh, "dh [T,F]")
-    d, F2 = _matrix(W_gate, "W_gate [d,F]")
+    d, _ = _matrix(W_gate, "W_gate [d,F]")
     ty = dh.dtype
     code = _code(rt, ty)
     pg = _tensor(W_gate, (d, F), ty, dh, "W_gate [d,F]")
