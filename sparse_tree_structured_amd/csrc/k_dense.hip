@@ -307,7 +307,7 @@ hipError_t split_operand(const void* x, int64_t rows, int64_t cols, int64_t ld, 
 // their time: the gated pair of 1514 x 3869 x
 // 1885 takes 77 us instead of 234, 2048 x 4095 x 2047 59 instead of 142.
 bool padding_wanted(const Product& p) {
-  if (!p.bf16) return false;
+  if (!p.bf16 || p.K == 0) return false;  // (gradients of no rows: zeros, and nothing to copy)
   const Padding pad = padding_of(p);
   if (!pad.a && !pad.b) return false;
   int64_t rows, cols;
