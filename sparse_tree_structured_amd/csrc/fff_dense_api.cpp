@@ -223,7 +223,9 @@ fff_status_t backward(const Shape& s, bool gated, const Backward& b, unsigned ch
   Product px = dx_product(s, gated), pw = dw_product(s, gated);
   const bool split = products && s.T > 0 && split_da(s, gated);
   if (split) {
-    px.bad = pw.bad = {reinterpret_cast<unsigned long long*>(ws + l.planes), fff::call_number()};
+    e = fff::start_word(ws + l.planes, stream, px.bad);
+    if (e != hipSuccess) return FFF_ERROR_HIP;
+    pw.bad = px.bad;
     give_planes(s, gated, ws + l.planes + 256, px, pw);
     if (!own_da) {
       e = fff::launch_split(b.dy, s.T, s.N, s.N, px.a_planes, px.bad, stream);

@@ -153,6 +153,11 @@ __global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t rows
   if (odd) *bad.word = bad.call;
 }
 
+// (no call has the number 0)
+__global__ __launch_bounds__(64) void clear_word_kernel(unsigned long long* word) {
+  if (threadIdx.x == 0) *word = 0;
+}
+
 // Copies x [rows, cols] bf16 to rows of `to_ld`, zeros behind the columns.
 __global__ __launch_bounds__(256) void pad_kernel(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
                                                   uint16_t* to, int64_t to_ld) {
@@ -242,6 +247,15 @@ hipError_t launch_split(const void* x, int64_t rows, int64_t cols, int64_t ld, c
   const int64_t blocks = ceil_div(rows * (out.ld / 8), 256);
   split_kernel<<<dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st>>>(
       static_cast<const float*>(x), rows, cols, ld, out, bad);
+  return hipGetLastError();
+}
+
+hipError_t start_word(void* at, hipStream_t st, NotFinite& out) {
+  out = {static_cast<unsigned long long*>(at), call_number()};
+  hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
+  const hipError_t asked = hipStreamIsCapturing(st, &capturing);
+  if (asked != hipSuccess || capturing == hipStreamCaptureStatusNone) return asked;
+  clear_word_kernel<<<dim3(1), dim3(64), 0, st>>>(out.word);
   return hipGetLastError();
 }
 
@@ -390,9 +404,8 @@ hipError_t launch_product(const Product& product, void* workspace, hipStream_t s
     const PlanesAt l = planes_at(p);
     hipError_t e = hipSuccess;
     int64_t rows, cols;
-    if (!p.bad.word)
-      p.bad = {reinterpret_cast<unsigned long long*>(ws + l.word), call_number()};
-    if (!p.a_planes.at) {
+    if (!p.bad.word) e = start_word(ws + l.word, st, p.bad);
+    if (e == hipSuccess && !p.a_planes.at) {
       a_sizes(p, rows, cols);
       e = split_operand(p.a, rows, cols, p.lda, ws + l.a, p.a_planes, p.bad, st);
     }

@@ -59,6 +59,11 @@ struct NotFinite {
   unsigned long long call;
 };
 unsigned long long call_number();  // one that no other call has
+// The word at `at` for a call on `st`, ahead of the launches that write it.
+// A captured call's number may be there from a replay before that met such a
+// value, so there a launch clears it: 4.5 us a replay (2048 x 1024 x 2048 93 us
+// instead of 89, 8191 x 767 x 2045 162 instead of 157.5).
+hipError_t start_word(void* at, hipStream_t st, NotFinite& out);
 
 struct Product {
   ProductKind kind;

@@ -36,3 +36,18 @@ def test_no_rows(record, ty):
         assert status == fff.SUCCESS, (name, s)
         dW = [k for k, _, _ in kernels if "product" in k]
         assert len(dW) == 1 and not [k for k, _, _ in kernels if "pad" in k or "split" in k], (name, s, kernels)
+
+
+def test_a_captured_call_clears_the_word_of_its_planes(record):
+    """Once, before any launch that writes or reads it; an eager call, whose
+    number is its own, does not, and nor do products without planes."""
+    sizes = {F32: (2048, 1024, 2048), BF16: (2048, 1024, 2048)}
+    for ty, (T, K, N) in sizes.items():
+        for small in (False, True):
+            s = shape(48 if small else T, K, N, ty, act=2)
+            calls = [(name, s, {}, captured) for name in R.ARGS for captured in (False, True)]
+            for (name, _, _, captured), (status, kernels) in zip(calls, record(calls)):
+                assert status == fff.SUCCESS
+                names = [k for k, _, _ in kernels]
+                cleared = [i for i, k in enumerate(names) if "clear_word" in k]
+                assert cleared == ([0] if captured and ty == F32 and not small else []), (name, ty, small, names)
