@@ -90,20 +90,25 @@ __device__ __forceinline__ void save_e4m3(const float (&v)[V], int n, uint8_t* c
     scales[static_cast<size_t>(row) * ((N + group - 1) / group) + col / group] = scale;
 }
 
-// V values into three planes, the first n of them stored; whether one is not
-// finite.  high is the nearest bf16 (towards zero where that would be
-// infinite), middle and low what is left, to nearest: high + middle + low is
-// the value where low is above bf16's smallest (values above 2^-110).
+// V values into three planes, the first n of them stored; whether one is
+// beyond the planes.  high is the nearest bf16, middle and low what is left,
+// to nearest: high + middle + low is the value where low is above bf16's
+// smallest (values above 2^-110), and off by at most 2^-134 below.
+//
+// Beyond are values that are not finite (infinity times a plane's zero would
+// be NaN) and those of 2^47 or more: with smaller ones every sum of the at
+// most 2^31 products stays below 2^125, whatever the terms' order and the
+// middle and low parts' signs.  With larger ones a sum that float32 has as
+// infinity could be infinity minus infinity.
+constexpr float kPlanesEnd = 0x1p47f;
 template <int V>
 __device__ __forceinline__ bool store_planes(const float (&v)[V], uint16_t* at, int64_t plane, int n) {
   float part[3][V];
   bool odd = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const bool finite = size_bits(v[i]) < 0x7f800000u;
-    odd |= !finite;
-    float h = bf16_to_f32(f32_to_bf16(v[i]));
-    if (size_bits(h) >= 0x7f800000u) h = __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+    odd |= size_bits(v[i]) >= __float_as_uint(kPlanesEnd);
+    const float h = bf16_to_f32(f32_to_bf16(v[i]));
     const float r = v[i] - h;
     const float m = bf16_to_f32(f32_to_bf16(r));
     part[0][i] = h;

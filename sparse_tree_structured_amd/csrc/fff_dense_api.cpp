@@ -149,7 +149,7 @@ Layout backward_layout(const Shape& s, bool gated) {
   l.da = take(gated ? 2 * rows * row : s.act != FFF_ACT_NONE ? rows * row : 0);
   l.x = take(s.x_dtype == FFF_DTYPE_E4M3 ? rows * fff::planes_ld(s.K) * e : 0);
   l.strips = take(gated ? 0 : fff::act_backward_partials(s.T, s.N, s.dtype == FFF_DTYPE_BF16) * 4);
-  // (the word of values that are not finite, then the planes)
+  // (the word of values beyond the planes, then the planes)
   l.planes = take(split_da(s, gated) ? 256 + (gated ? 2 : 1) * fff::planes_bytes(s.T, s.N) : 0);
   Product px = dx_product(s, gated), pw = dw_product(s, gated);
   give_planes(s, gated, nullptr, px, pw);

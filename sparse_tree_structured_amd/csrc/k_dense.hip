@@ -10,7 +10,7 @@ namespace {
 template <class Epi>
 __global__ __launch_bounds__(256) void sum_slices_kernel(const float* partial, int slices,
                                                          int products, int64_t M, int N, Epi epi,
-                                                         NotFinite bad) {
+                                                         BeyondPlanes bad) {
   if (bad.word && *bad.word == bad.call) return;
   const int lane = threadIdx.x & (kWave - 1);
   const int strips = (N + 255) / 256;
@@ -133,7 +133,7 @@ Cut cut_any(const Product& p, double* us_of = nullptr) {
 // Splits of x [rows, cols] float32 into planes: a lane has eight columns, the
 // row's padding among them.
 __global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t rows, int64_t cols, int64_t ld,
-                                                    Planes out, NotFinite bad) {
+                                                    Planes out, BeyondPlanes bad) {
   const int64_t pieces = out.ld / 8;
   bool odd = false;
   for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < rows * pieces;
@@ -203,7 +203,7 @@ size_t cut_bytes(const Product& p, const Cut& c) {
 
 template <class Epi>
 hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int N, const Epi& epi,
-                             const NotFinite& bad, hipStream_t st) {
+                             const BeyondPlanes& bad, hipStream_t st) {
   const int64_t units = M * ceil_div(N, 256) * (Epi::kGated ? 1 : c.products);
   const int64_t blocks = ceil_div(units, 4);
   sum_slices_kernel<Epi><<<dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
@@ -212,7 +212,7 @@ hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int 
 }
 #define FFF_SUM(E)                                                                                \
   template hipError_t launch_sum_slices<E>(const float*, const Cut&, int64_t, int, const E&, \
-                                           const NotFinite&, hipStream_t)
+                                           const BeyondPlanes&, hipStream_t)
 FFF_SUM(GatedEpilogue<uint16_t>);
 FFF_SUM(GatedEpilogue<float>);
 using LinearBf16 = LinearEpilogue<uint16_t, uint16_t>;
@@ -243,14 +243,14 @@ bool split_wanted(const Product& p) {
 }
 
 hipError_t launch_split(const void* x, int64_t rows, int64_t cols, int64_t ld, const Planes& out,
-                        const NotFinite& bad, hipStream_t st) {
+                        const BeyondPlanes& bad, hipStream_t st) {
   const int64_t blocks = ceil_div(rows * (out.ld / 8), 256);
   split_kernel<<<dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st>>>(
       static_cast<const float*>(x), rows, cols, ld, out, bad);
   return hipGetLastError();
 }
 
-hipError_t start_word(void* at, hipStream_t st, NotFinite& out) {
+hipError_t start_word(void* at, hipStream_t st, BeyondPlanes& out) {
   out = {static_cast<unsigned long long*>(at), call_number()};
   hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
   const hipError_t asked = hipStreamIsCapturing(st, &capturing);
@@ -312,7 +312,7 @@ PlanesAt planes_at(const Product& p) {
 }
 
 hipError_t split_operand(const void* x, int64_t rows, int64_t cols, int64_t ld, unsigned char* to,
-                         Planes& out, const NotFinite& bad, hipStream_t st) {
+                         Planes& out, const BeyondPlanes& bad, hipStream_t st) {
   out = {to, planes_ld(cols), rows * planes_ld(cols)};
   return launch_split(x, rows, cols, ld, out, bad, st);
 }

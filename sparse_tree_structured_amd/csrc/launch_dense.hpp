@@ -53,8 +53,9 @@ inline size_t planes_bytes(int64_t rows, int64_t cols) {
   return 3 * size_t(rows) * size_t(planes_ld(cols)) * 2;
 }
 
-// A word that holds the call's number once a value that is not finite was met.
-struct NotFinite {
+// A word that holds the call's number once a value was met that planes do not
+// take: one that is not finite, or of 2^47 or more in size.
+struct BeyondPlanes {
   unsigned long long* word;  // null: not asked
   unsigned long long call;
 };
@@ -63,7 +64,7 @@ unsigned long long call_number();  // one that no other call has
 // A captured call's number may be there from a replay before that met such a
 // value, so there a launch clears it: 4.5 us a replay (2048 x 1024 x 2048 93 us
 // instead of 89, 8191 x 767 x 2045 162 instead of 157.5).
-hipError_t start_word(void* at, hipStream_t st, NotFinite& out);
+hipError_t start_word(void* at, hipStream_t st, BeyondPlanes& out);
 
 struct Product {
   ProductKind kind;
@@ -77,12 +78,12 @@ struct Product {
   int N;
   int64_t K;      // of one product
   Epilogue e;
-  // float32 operands in planes (split_wanted), and whether all are finite: the
-  // kernel on planes runs if they are, the other one if not.  at of both
+  // float32 operands in planes (split_wanted), and whether one has a value beyond
+  // them: the kernel on planes runs if none has, else the other one.  at of both
   // pairs' planes; the second A's follow the first's a_planes_second later.
   Planes a_planes, b_planes[2];
   int64_t a_planes_second;
-  NotFinite bad;
+  BeyondPlanes bad;
   bool padded;  // bf16: the rows have zeros up to whole 16-byte pieces
 };
 
@@ -90,7 +91,7 @@ struct Product {
 bool split_wanted(const Product& p);
 // x, rows of ld floats, cols of them there, into planes.
 hipError_t launch_split(const void* x, int64_t rows, int64_t cols, int64_t ld, const Planes& out,
-                        const NotFinite& bad, hipStream_t st);
+                        const BeyondPlanes& bad, hipStream_t st);
 
 // Whether its tiles fit one launch.
 bool product_fits(const Product& p);
@@ -127,7 +128,7 @@ struct ActBackward {
   float* dbias;           // [N] sums over rows of da, or null
   float* partial;         // workspace of dbias
   Planes da_planes[2];    // float32: da (gated: the gate's and up's) once more in planes, or none
-  NotFinite bad;
+  BeyondPlanes bad;
   Restore x;
 };
 size_t act_backward_partials(int64_t T, int N, bool bf16);  // floats

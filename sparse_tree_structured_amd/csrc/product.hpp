@@ -34,7 +34,7 @@ using TileSmall = StepCfg<128, 128, 64, 64, 3>;  // two workgroups a compute uni
 // The slices' sums through the epilogue (nothing where `bad` holds the call's number).
 template <class Epi>
 hipError_t launch_sum_slices(const float* partial, const Cut& c, int64_t M, int N, const Epi& epi,
-                             const NotFinite& bad, hipStream_t st);
+                             const BeyondPlanes& bad, hipStream_t st);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -95,7 +95,7 @@ hipError_t run_with(const Product& p, const Epi& epi, void* workspace, hipStream
     e = launch_cut<E, KIND, PAIR>(p, part, c, st);
     if (e == hipSuccess) e = launch_sum_slices(part.partial, c, p.M, p.N, epi, p.bad, st);
   }
-  // On planes: the kernel on the values themselves, should they not be finite.
+  // On planes: the kernel on the values themselves, should one be beyond them.
   if (e == hipSuccess && p.bad.word)
     e = launch_cut<E, KIND, PAIR>(p, epi, cut_whole(p), st);
   return e;
