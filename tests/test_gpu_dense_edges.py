@@ -1,6 +1,7 @@
 """The dense feed-forward operators at the edges of what their header allows:
 no rows, replays of a captured call, values at the ends of float32's
-range (bounds: dense_oracle.py)."""
+range, operands anywhere in memory, the workspace's end (bounds:
+dense_oracle.py)."""
 import math
 
 import pytest
@@ -8,7 +9,7 @@ import torch
 
 import dense_oracle as O
 import sparse_tree_structured_amd as fff
-from test_gpu_dense import DEV, TY, d64, randn, say, seeded
+from test_gpu_dense import DEV, TY, U, d64, randn, say, seeded
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +118,113 @@ def test_the_planes_range(power):
         if power < 0:
             bound = bound + 2.0 ** -134 * (d64(xs).abs().sum(1, keepdim=True) + d64(Ws).abs().sum(0, keepdim=True))
         O.close(fff.linear(xs, Ws).y, want, bound + want.abs() * O.U32 + O.TINY, (a, b))
+
+
+def odd(t):
+    """A view with t's values that starts one element into a buffer."""
+    buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device=t.device)
+    v = buf[1:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,N", [(33, 72, 136), (257, 41, 77), (300, 64, 256), (1200, 264, 1032), (2048, 1024, 2048)])
+def test_every_output_of_operands_at_odd_addresses(T, K, N, ty):
+    """All outputs against float64, at widths of whole 16-byte pieces among
+    others, whose tiles would go straight into LDS if they were aligned."""
+    gen = seeded("odd", T, K, N)
+    say("odd addresses", T, K, N, ty)
+    x, dy = odd(randn(gen, T, K, ty=ty)), odd(randn(gen, T, N, ty=ty))
+    W, V = (odd(randn(gen, K, N, ty=ty, size=1 / math.sqrt(K))) for _ in range(2))
+    gate, up = (odd(randn(gen, T, N, ty=ty, size=2.0)) for _ in range(2))
+    kept = [fff.checkpoint(t, g) for t, g in ((x, 32), (gate, 64), (up, 64))]
+    kept = [fff.Checkpoint(odd(c.codes.view(torch.uint8)).view(c.codes.dtype), odd(c.scale), c.group) for c in kept]
+
+    def out(*shape, f32=False):
+        return odd(torch.zeros(*shape, dtype=torch.float32 if f32 else TY[ty], device=DEV))
+
+    u, f = U[ty], O.U32
+    y = fff.linear(x, W, act="silu", y=out(T, N)).y
+    want, e = O.linear(d64(x), d64(W), None, None, "silu")[2:]
+    O.close(y, want, e + (want.abs() + e) * u, "y")
+    h = fff.gated(x, W, V, h=out(T, N)).h
+    want, e = O.gated(d64(x), d64(W), d64(V), "silu")[4:]
+    O.close(h, want, e + (want.abs() + e) * u, "h")
+    o = fff.linear_backward(dy, x, W, dx=out(T, K), dW=out(K, N, f32=True), dbias=out(N, f32=True))
+    want, e = O.product(d64(dy), d64(W).t())
+    O.close(o.dx, want, e + (want.abs() + e) * u, "dx")
+    want, e = O.product(d64(x).t(), d64(dy))
+    O.close(o.dW, want, e + (want.abs() + e) * f, "dW")
+    O.close(o.dbias, d64(dy).sum(0), O.sum_u(T) * d64(dy).abs().sum(0), "dbias")
+    for keep in (False, True):
+        a, b, c = kept if keep else (x, gate, up)
+        xv, g, w = (O.load(t.codes, t.scale, t.group) if keep else d64(t) for t in (a, b, c))
+        o = fff.gated_backward(dy, a, W, V, b, c, dx=out(T, K), dW_gate=out(K, N, f32=True),
+                               dW_up=out(K, N, f32=True), h=out(T, N))
+        value, slope, ev, es = O.activation(g, "silu")
+        d = d64(dy)
+        dg, du = d * w * slope, d * value
+        eg = (d * w).abs() * es + dg.abs() * 3 * f
+        eu = d.abs() * ev + du.abs() * 2 * f
+        eg, eu = eg + (dg.abs() + eg) * u, eu + (du.abs() + eu) * u
+        want, e = O.product(torch.cat([dg, du], 1), torch.cat([d64(W), d64(V)], 1).t(), torch.cat([eg, eu], 1))
+        O.close(o.dx, want, e + (want.abs() + e) * u, "the pair's dx")
+        ex = xv.t().abs() * u if keep and ty == "bf16" else None
+        for got, da, ea, what in ((o.dW_gate, dg, eg, "dW_gate"), (o.dW_up, du, eu, "dW_up")):
+            want, e = O.product(xv.t(), da, ex, ea)
+            O.close(got, want, e + (want.abs() + e) * f, what)
+        e = ev * w.abs() + (value * w).abs() * 2 * f
+        O.close(o.h, value * w, e + ((value * w).abs() + e) * u, "h made again")
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 264), (40, 1000, 96), (70, 96, 200), (257, 41, 77), (520, 1032, 1160),
+                                   (1000, 1023, 1537), (2048, 1024, 2048)])
+def test_a_workspace_of_the_queried_size(T, K, N, ty):
+    """Calls on workspaces of just the bytes asked for, full of NaN: the values
+    of calls on their own ones, and nothing behind the end is written.  dW is
+    the same with and without dx."""
+    gen = seeded("workspace", T, K, N)
+    say("workspaces", T, K, N, ty)
+    x, dy, W, V = (randn(gen, *s, ty=ty) for s in ((T, K), (T, N), (K, N), (K, N)))
+    x8 = fff.checkpoint(x, 64)
+    code = {"f32": fff.DTYPE_F32, "bf16": fff.DTYPE_BF16}[ty]
+    space = torch.full((1 << 28,), 255, dtype=torch.uint8, device=DEV)
+
+    def shape(save=None, act="none", x_kept=False):
+        return (T, K, N, code, code, fff.ACTS[act], fff.DTYPE_E4M3 if save else code, save or 0,
+                fff.DTYPE_E4M3 if x_kept else code, 64 if x_kept else 0)
+
+    def run(name, sizes, call):
+        need = fff._dense(name, *sizes)[1]
+        want = call(None)
+        got = call(space[:need])
+        torch.cuda.synchronize()
+        assert bool((space[need:] == 255).all()), name
+        space[:need] = 255
+        for a, b in zip(want, got):
+            if a is not None:
+                assert torch.equal(a.float(), b.float()), name
+
+    def flat(o):
+        return [t for part in o for t in ((part.codes, part.scale) if isinstance(part, fff.Checkpoint) else (part,))]
+
+    a = fff.linear(x, W, act="gelu", save="e4m3", group=32)
+    b = fff.gated(x, W, V, save="e4m3", group=128)
+    run("fff_linear", shape() + (code,), lambda ws: fff.linear(x, W, workspace=ws))
+    run("fff_linear", shape(32, "gelu") + (code,),
+        lambda ws: flat(fff.linear(x, W, act="gelu", save="e4m3", group=32, workspace=ws)))
+    run("fff_gated", shape(128, "silu") + (code,),
+        lambda ws: flat(fff.gated(x, W, V, save="e4m3", group=128, workspace=ws)))
+    back = dict(want_dbias=True, grad_dtype=TY[ty])
+    run("fff_linear_backward", shape() + (code,), lambda ws: fff.linear_backward(dy, x, W, workspace=ws, **back))
+    for grads in (dict(), dict(want_dx=False), dict(want_dW=False)):
+        run("fff_linear_backward", shape(32, "gelu", True) + (code,),
+            lambda ws: fff.linear_backward(dy, x8, W, act="gelu", pre=a.pre, workspace=ws, **back, **grads))
+        run("fff_gated_backward", shape(128, "silu", True) + (code,),
+            lambda ws: fff.gated_backward(dy, x8, W, V, b.gate, b.up, want_h=True, grad_dtype=TY[ty], workspace=ws,
+                                          **grads))
+    both = fff.gated_backward(dy, x, W, V, b.gate, b.up)
+    assert torch.equal(both.dW_up, fff.gated_backward(dy, x, W, V, b.gate, b.up, want_dx=False).dW_up)
+    assert torch.equal(both.dx, fff.gated_backward(dy, None, W, V, b.gate, b.up, want_dW=False).dx)
