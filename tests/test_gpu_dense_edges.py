@@ -1,7 +1,8 @@
 """The dense feed-forward operators at the edges of what their header allows:
-no rows, replays of a captured call, values at the ends of float32's
-range, operands anywhere in memory, the workspace's end (bounds:
-dense_oracle.py)."""
+no rows, replays of a captured call, values at the ends of float32's range,
+operands anywhere in memory, the workspace's end, calls from several threads,
+offsets past 2^31 (bounds: dense_oracle.py)."""
+import concurrent.futures
 import math
 
 import pytest
@@ -228,3 +229,69 @@ def test_a_workspace_of_the_queried_size(T, K, N, ty):
     both = fff.gated_backward(dy, x, W, V, b.gate, b.up)
     assert torch.equal(both.dW_up, fff.gated_backward(dy, x, W, V, b.gate, b.up, want_dx=False).dW_up)
     assert torch.equal(both.dx, fff.gated_backward(dy, None, W, V, b.gate, b.up, want_dW=False).dx)
+
+
+def test_calls_of_several_host_threads():
+    """One stream and one size to a thread, small and large ones, each again and
+    again beside the others: the values of calls by themselves."""
+    say("host threads")
+    sizes = [(3, 4096, 512, "bf16"), (64, 2048, 768, "f32"), (600, 264, 136, "bf16"), (2048, 1024, 2048, "f32")]
+    work = []
+    for T, K, N, ty in sizes:
+        gen = seeded("threads", T, K, N)
+        x, W, dy = randn(gen, T, K, ty=ty), randn(gen, K, N, ty=ty), randn(gen, T, N, ty=ty)
+
+        def calls(stream=None, x=x, W=W, dy=dy):
+            g = fff.gated(x, W, W, save="same", stream=stream)
+            return [fff.linear(x, W, residual=dy, act="silu", stream=stream).y, g.h,
+                    *fff.gated_backward(dy, x, W, W, g.gate, g.up, want_h=True, stream=stream)]
+
+        work.append((calls, calls(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def many(item):
+        calls, want, stream = item
+        got = [calls(stream) for _ in range(20)]
+        stream.synchronize()
+        return all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+    with concurrent.futures.ThreadPoolExecutor(len(work)) as pool:
+        assert all(pool.map(many, work))
+
+
+def test_offsets_past_32_bits_on_planes():
+    """Large float32 products whose operands, planes among them, have elements
+    past 2^31: rows at the end against calls on them alone, sums over all rows
+    against those over two parts of them."""
+    T, K, N = (1 << 20) + 300, 512, 2056
+    gen = seeded("planes past 2^31")
+    say("planes past 2^31")
+    assert T * N > 1 << 31
+    dh, gate = (torch.randn(T, N, generator=gen, device=DEV) for _ in range(2))
+    x, W, V = randn(gen, T, K), randn(gen, K, N, size=N ** -0.5), randn(gen, K, N, size=N ** -0.5)
+    o = fff.gated_backward(dh, x, W, V, gate, gate, act="relu", want_h=True)
+    tail = slice(T - 300, T)
+    c = [t[tail].clone() for t in (dh, x, gate)]
+    p = fff.gated_backward(c[0], c[1], W, V, c[2], c[2], act="relu", want_h=True)
+    assert torch.equal(o.h[tail], p.h)
+    dg, du = c[0] * c[2] * (c[2] > 0), c[0] * c[2].clamp(min=0)
+    size = d64(dg).abs() @ d64(W).abs().t() + d64(du).abs() @ d64(V).abs().t()
+    O.close(o.dx[tail], d64(p.dx), 2 * O.sum_u(2 * N) * size, "dx")
+    parts, half = [], T // 2
+    for rows in (slice(0, half), slice(half, T)):
+        q = fff.gated_backward(dh[rows], x[rows], W, V, gate[rows], gate[rows], act="relu", want_dx=False)
+        parts.append((d64(q.dW_gate), d64(q.dW_up)))
+    for k, got in enumerate((o.dW_gate, o.dW_up)):
+        da = dh * gate.clamp(min=0)  # (relu with the gate as up: dg = du)
+        size = x.abs().t() @ da.abs_()
+        del da
+        O.close(got, parts[0][k] + parts[1][k], 2.1 * O.sum_u(T) * d64(size), ("dW_gate", "dW_up")[k])
+    del o, p, q, gate, parts, size
+    B = W.t().contiguous()
+    y = fff.linear(dh, B, residual=x).y
+    want, e = O.product(d64(c[0]), d64(B))
+    want = want + d64(c[1])
+    O.close(y[tail], want, e + want.abs() * 2 * O.U32, "y")
+    O.close(y[tail], d64(fff.linear(c[0], B, residual=c[1]).y), 2 * e + want.abs() * 4 * O.U32, "y of the rows alone")
+    del dh, y, x
+    torch.cuda.empty_cache()
