@@ -576,7 +576,8 @@ fff_status_t fff_grad_norm(const fff_adamw_tensor_t *tensors, int64_t count, dou
  * bias, activation and residual in its epilogue, the gated pair of
  * projections, the backward passes of both, and activations kept for them in
  * 8 bits.  The rules above hold: dense row-major device tensors, caller-owned
- * workspaces, no state, validation before any HIP call.  Pointers need an
+ * workspaces, validation before any HIP call, no state (but a counter in the
+ * host's memory that gives calls their numbers).  Pointers need an
  * element's alignment only (workspaces 256 bytes); bf16 tensors of 16-byte
  * alignment whose widths are multiples of 8 take the fastest kernels.
  *
@@ -587,9 +588,12 @@ fff_status_t fff_grad_norm(const fff_adamw_tensor_t *tensors, int64_t count, dou
  *   NONE a     GELU a q(2 sqrt(2/pi) (a + 0.044715 a^3)) (the tanh form)
  *   SILU a q(a)     RELU max(a, 0)          with q(z) = 1 / (1 + exp(-z))
  * Sums and activations are in 32 bits and outputs rounded once; bf16 products
- * are exact, float32 ones rounded to 32 bits.  a, or g and u, can be kept for
- * the backward pass as they are before the activation, in the layer's type
- * or in 8 bits.
+ * are exact, float32 ones rounded to 32 bits.  Large float32 products are made
+ * of bf16 parts, three of each operand, as exact for operands of 2^-110 to
+ * 2^47 in size.  A smaller value is off by up to 2^-134; with a larger one, an
+ * infinity or NaN in an operand the float32 kernel makes the product, at about
+ * half the rate.  a, or g and u, can be kept for the backward pass as they are
+ * before the activation, in the layer's type or in 8 bits.
  *
  * 8 bits (FFF_DTYPE_E4M3) are those of fff_rms_norm: a float32 scale for every
  * row (group 0) or every `group` columns of one (32, 64 or 128; the last group
@@ -644,7 +648,9 @@ typedef struct fff_dense_shape {
  *   pre       [T,N] save_dtype: a, or NULL
  *   pre_scale [T, ceil(N / save_group)] float32; E4M3 only
  * y may be the buffer of the residual; no other overlap is allowed.  T = 0 is
- * a no-op.  Results are the same on every call (no atomics).
+ * a no-op.  Results are the same on every call of a shape and alignment,
+ * captured or not: sums are added in a fixed order.  (Where the workgroups of a
+ * few rows' product meet, atomics say which have arrived, and nothing else.)
  */
 fff_status_t fff_linear_workspace_size(const fff_dense_shape_t *shape, size_t *bytes);
 fff_status_t fff_linear(const fff_dense_shape_t *shape, const void *x, const void *W,
@@ -674,9 +680,11 @@ fff_status_t fff_linear_backward(const fff_dense_shape_t *shape, const void *dy,
  *   h         [T,N] dtype
  *   gate, up  [T,N] save_dtype: g and u, each or NULL, with gate_scale and
  *             up_scale [T, ceil(N / save_group)] float32 for E4M3
- * Both projections, the activation and the product are one kernel (and a sum
- * of its parts where K is cut for small T).  No overlap is allowed.  T = 0 is
- * a no-op.
+ * Both projections, the activation and the product are one kernel.  Launches
+ * beside it: a sum of its parts where K is cut; copies of operands whose bf16
+ * rows are odd; for large float32 products the operands' bf16 parts, and the
+ * float32 kernel, which leaves at once where the parts were used.  No overlap
+ * is allowed.  T = 0 is a no-op.
  */
 fff_status_t fff_gated_workspace_size(const fff_dense_shape_t *shape, size_t *bytes);
 fff_status_t fff_gated(const fff_dense_shape_t *shape, const void *x, const void *W_gate,

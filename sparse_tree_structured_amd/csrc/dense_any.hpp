@@ -9,9 +9,12 @@
 //
 // Float32 is bound by its matrix operations (a compute unit's 128 x 256 x 16
 // step takes 1.9 us at full rate): 16384 x 8192 x 2048 runs at 120 TFLOP/s.
-// bf16 steps of 32 take 1.2 us, most of it addresses and guards, 0.9 PFLOP/s at
-// best: bf16 comes here where rows are not aligned and copies are not worth
-// their time.  Two steps' loads in registers changed nothing.
+// bf16 steps of 32 take 0.75 to 0.8 us, most of it addresses and guards, where
+// rows are whole 16-byte pieces at odd addresses (16384 x 8192 x 2048 814 us, 0.68
+// PFLOP/s; 483 aligned, straight into LDS), and 0.7 to 1.3 us with odd rows (16384
+// x 2047 x 8191 743 us, 4096 x 4095 x 4095 327; 513 and 137 with copies, straight
+// into LDS): bf16 comes here where pointers are not aligned, or rows are odd and
+// copies are not worth their time.  Two steps' loads in registers changed nothing.
 #pragma once
 
 #include "dense.hpp"

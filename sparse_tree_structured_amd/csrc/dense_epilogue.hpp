@@ -8,7 +8,11 @@
 // four columns a lane at a time: at 16384 x 2048 x 8192 its 8-bit saves cost
 // 257 us of 1239 (five steps over lanes and a scale for every four columns;
 // here one step and a scale for 16; 1056 in all), and at 16384 x 2048 x 16384
-// its plain outputs 160 us of 1040 (here 60).
+// its plain outputs 160 us of 1040 (here 60).  A linear layer whose sums are
+// kept, or whose output is in 32 bits, and products on planes still take it:
+// 16384 x 2048 x 8192 with bias and GELU takes 541 us, and keeping its sums 627
+// (in the layer's type) or 677 (in 8 bits); without them but with a 32-bit
+// residual and output 658.
 #pragma once
 
 #include "dense.hpp"

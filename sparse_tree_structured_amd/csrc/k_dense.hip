@@ -63,8 +63,9 @@ struct TileSize {
 // The time of a product in one kind of tile and number of slices, in us: what
 // the busiest compute unit does, a start and an epilogue for each of its
 // tiles, and for slices a second launch and the sums' way through memory.
-// The rates are those measured on one tile's work with the chip full; what the
-// model chooses in bf16, as measured (us): 512 x 2048 x 1024 12.4, 1024 x 2048
+// The rates are those measured on one tile's work with the chip full; that of the
+// register-staged bf16 tile (1.5 us a step) is of few tiles of odd rows, where it
+// decides whether to copy.  What the model chooses in bf16, as measured (us): 512 x 2048 x 1024 12.4, 1024 x 2048
 // x 4096 31, 2048 x 2048 x 4096 44, 4096 x 2048 x 4096 64 (1.07 PFLOP/s).
 double time_of(const Product& p, const TileSize& t, int64_t tiles, int64_t total, int64_t slices) {
   const int64_t steps = ceil_div(total, slices);
@@ -318,8 +319,8 @@ hipError_t split_operand(const void* x, int64_t rows, int64_t cols, int64_t ld, 
 }
 
 // Whether copies with padded rows, for the tiles straight into LDS, are worth
-// their time: the gated pair of 1514 x 3869 x
-// 1885 takes 77 us instead of 234, 2048 x 4095 x 2047 59 instead of 142.
+// their time: 2048 x 4095 x 2047 takes 61 us instead of 137 (the gated pair 88
+// instead of 245), 512 x 767 x 2045 20 instead of 23; 128 x 767 x 2045 18 either way.
 bool padding_wanted(const Product& p) {
   if (!p.bf16 || p.K == 0) return false;  // (gradients of no rows: zeros, and nothing to copy)
   const Padding pad = padding_of(p);

@@ -87,6 +87,12 @@ int strip_rows(int64_t T, int64_t col_blocks) {
 }
 constexpr int64_t kMaxStrips = 1024;  // a workgroup takes more than one, then
 
+// In bf16 da and an x that is read back are rounded to bf16 here, once, for
+// they are the next products' operands: each moves a gradient by up to 2^-8 of
+// its terms' sizes.  (dW in bf16 from 8 bits is off by 0.29 % of its size in all,
+// 0.17 with its own rounding alone.  An operand in two bf16 parts would double
+// the products' time, nine tenths of the pass.)
+//
 // da = dy act'(pre); of the gated pair dgate = dh up act'(gate) and dup = dh
 // act(gate), h = act(gate) up.  A workgroup has 64 lanes of columns and a
 // strip of rows; column sums are added over its rows in order, then over its
