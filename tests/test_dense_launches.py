@@ -1,4 +1,7 @@
 """What the dense block's entry points launch, on the CPU (launch_recorder.py)."""
+import math
+import random
+
 import pytest
 
 import launch_recorder as R
@@ -51,3 +54,37 @@ def test_a_captured_call_clears_the_word_of_its_planes(record):
                 names = [k for k, _, _ in kernels]
                 cleared = [i for i, k in enumerate(names) if "clear_word" in k]
                 assert cleared == ([0] if captured and ty == F32 and not small else []), (name, ty, small, names)
+
+
+def test_every_shape_launches_or_is_refused(record):
+    """Shapes over the whole range (widths up to 2^20, rows up to 2^31 - 1), operands
+    aligned and not, outputs asked for and not: a launch never has no workgroups
+    or more threads than HIP takes."""
+    rng = random.Random(7)
+
+    def log(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    calls = []
+    while len(calls) < 3000:
+        ty, step, name = rng.choice([F32, BF16]), rng.choice([1, 8]), rng.choice(sorted(R.ARGS))
+        T = rng.choice([0, 1, log(1, 64), log(64, 40000), log(1, 2 ** 31 - 1)])
+        K, N = (step * log(1, (1 << 20) // step) for _ in range(2))
+        if max(T * K, T * N, K * N) >= 1 << 40:
+            continue
+        back = "backward" in name
+        save, x = (rng.choice([ty, E4M3]) for _ in range(2))
+        s = shape(T, K, N, ty, act=rng.randrange(4), save_dtype=save,
+                  save_group=rng.choice([32, 64, 128]) if save == E4M3 else 0, grad_dtype=rng.choice([ty, F32]))
+        if back:
+            s.update(x_dtype=x, x_group=rng.choice([0, 32, 64, 128]) if x == E4M3 else 0)
+        elif name == "fff_linear":
+            s.update(out_dtype=rng.choice([ty, F32]))
+        p = {k: (1 << 40) + 4 for k in ("x", "W", "Wg", "Wu", "dy", "dh") if rng.random() < 0.2}
+        may_be_none = ["dx", "dbias"] if back else ["bias", "residual", "pre", "gate", "up"]
+        p.update({k: 0 for k in may_be_none if rng.random() < 0.3})
+        if back and rng.random() < 0.3:
+            p.update(dW=0, dWg=0, dWu=0)
+        calls.append((name, s, p, rng.random() < 0.2))
+    for call, (status, _) in zip(calls, record(calls)):
+        assert status in (fff.SUCCESS, fff.ERROR_NOT_SUPPORTED), call

@@ -1,7 +1,7 @@
 """The dense feed-forward operators at the edges of what their header allows:
 no rows, replays of a captured call, values at the ends of float32's range,
 operands anywhere in memory, the workspace's end, calls from several threads,
-offsets past 2^31 (bounds: dense_oracle.py)."""
+offsets past 2^31, the widest and the longest sizes (bounds: dense_oracle.py)."""
 import concurrent.futures
 import math
 
@@ -10,7 +10,8 @@ import torch
 
 import dense_oracle as O
 import sparse_tree_structured_amd as fff
-from test_gpu_dense import DEV, TY, U, d64, randn, say, seeded
+from test_gpu_dense import (DEV, TY, U, check_gated, check_gated_back, check_linear, check_linear_back, d64, randn, say,
+                            seeded)
 
 pytestmark = pytest.mark.gpu
 
@@ -295,3 +296,13 @@ def test_offsets_past_32_bits_on_planes():
     O.close(y[tail], d64(fff.linear(c[0], B, residual=c[1]).y), 2 * e + want.abs() * 4 * O.U32, "y of the rows alone")
     del dh, y, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,N", [(1, 1 << 20, 8), (1, 8, 1 << 20), (70, (1 << 20) - 1, 40), (70, 40, (1 << 20) - 1),
+                                   ((1 << 20) + 3, 3, 2)])
+def test_the_widest_and_the_longest(T, K, N, ty):
+    check_linear(T, K, N, ty, ty, act="silu", bias=True, save="e4m3", group=32)
+    check_gated(T, K, N, ty)
+    check_linear_back(T, K, N, ty, act="gelu", group=32, x_group=0)
+    check_gated_back(T, K, N, ty, group=64, x_group=32)
